@@ -32,9 +32,12 @@ EXPORTS = ("gdn_prefill", "gdn_prefill_noalloc", "gdn_noalloc_scratch_bytes", "k
            "kda_prefill_batched", "kda_prefill_varlen", "gdn_decode", "kda_decode",
            "gdn_chunk_table", "gdn_profile_enable", "gdn_profile_read", "gdn_workspace_bytes",
            "gdn_segments", "gdn_segment_plan", "gdn_status_string", "gdn_debug_validate",
-           "gdn_debug_flag_polls")
+           "gdn_debug_flag_polls", "gdn_draft", "kda_draft", "gdn_fold", "kda_fold",
+           "gdn_verify", "gdn_verify_workspace_bytes")
 GDN_BAD_CU_START, GDN_BAD_CU_ORDER, GDN_BAD_CU_TOTAL, GDN_BAD_CU_MAXLEN = 1, 2, 4, 8
 GDN_BAD_KDA_GATE = 16
+GDN_BAD_TAPE = 32
+GDN_DRAFT_MAX_T = 16
 GDN_PROF_FRONT = 0
 GDN_PROF_RECUR = 1
 GDN_PROF_STATE = 2
@@ -51,11 +54,17 @@ class gdn_params(ctypes.Structure):
                 ("norm_eps", ctypes.c_float), ("Hqk", ctypes.c_int32)]
 
 
+class gdn_tape(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("d", ctypes.c_void_p), ("g", ctypes.c_void_p),
+                ("raw", ctypes.c_void_p), ("len", ctypes.c_void_p), ("cap", ctypes.c_int32)]
+
+
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
 _sz = ctypes.c_size_t
 _pp = ctypes.POINTER(gdn_params)
+_tp = ctypes.POINTER(gdn_tape)
 _lock = threading.Lock()
 _lib = None
 
@@ -86,6 +95,16 @@ def load(path: str = SO):
         decode = [_pp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp]
         lib.gdn_decode.argtypes = decode
         lib.kda_decode.argtypes = decode
+        draft = [_pp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _tp, _vp, _i32, _i32, _i32, _vp]
+        lib.gdn_draft.argtypes = draft
+        lib.kda_draft.argtypes = draft
+        fold = [_pp, _vp, _vp, _vp, _vp, _tp, _vp, _i32, _i32, _i32, _vp]
+        lib.gdn_fold.argtypes = fold
+        lib.kda_fold.argtypes = fold
+        lib.gdn_verify.argtypes = [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _i32, _i32, _i32,
+                                   _vp, _vp, _vp, _vp, _sz, _vp]
+        lib.gdn_verify_workspace_bytes.argtypes = [_i32, _i32, _i32]
+        lib.gdn_verify_workspace_bytes.restype = _sz
         lib.gdn_chunk_table.argtypes = [_vp, _i32, _i32, _vp, _i64, _vp, _vp]
         lib.gdn_profile_enable.argtypes = [ctypes.c_int]
         lib.gdn_profile_enable.restype = ctypes.c_int
@@ -105,7 +124,8 @@ def load(path: str = SO):
         lib.gdn_status_string.restype = ctypes.c_char_p
         for name in ("gdn_prefill", "kda_prefill", "gdn_prefill_batched",
                      "gdn_prefill_varlen", "kda_prefill_batched", "kda_prefill_varlen",
-                     "gdn_decode", "kda_decode", "gdn_chunk_table"):
+                     "gdn_decode", "kda_decode", "gdn_chunk_table", "gdn_draft", "kda_draft",
+                     "gdn_fold", "kda_fold", "gdn_verify"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -192,6 +212,51 @@ def gdn_decode(p, q, k, v, g, beta, h_ptrs, conv_state_ptrs, conv_w, o, B, strea
 def kda_decode(p, q, k, v, g, beta, h_ptrs, conv_state_ptrs, conv_w, o, B, stream):
     return load().kda_decode(ctypes.byref(p), _p(q), _p(k), _p(v), _p(g), _p(beta),
                              _p(h_ptrs), _p(conv_state_ptrs), _p(conv_w), _p(o), B, stream)
+
+
+def tape(k, d, g, raw, len, cap):
+    """A gdn_tape struct over device tensors or pointers (raw None without the conv). It
+    holds no references: the tensors must outlive its use."""
+    return gdn_tape(_p(k), _p(d), _p(g), _p(raw), _p(len), cap)
+
+
+def gdn_draft(p, q, k, v, g, beta, h_ptrs, conv_state_ptrs, conv_w, tape, o, B, T, share,
+              stream):
+    return load().gdn_draft(ctypes.byref(p), _p(q), _p(k), _p(v), _p(g), _p(beta),
+                            _p(h_ptrs), _p(conv_state_ptrs), _p(conv_w), ctypes.byref(tape),
+                            _p(o), B, T, share, stream)
+
+
+def kda_draft(p, q, k, v, g, beta, h_ptrs, conv_state_ptrs, conv_w, tape, o, B, T, share,
+              stream):
+    return load().kda_draft(ctypes.byref(p), _p(q), _p(k), _p(v), _p(g), _p(beta),
+                            _p(h_ptrs), _p(conv_state_ptrs), _p(conv_w), ctypes.byref(tape),
+                            _p(o), B, T, share, stream)
+
+
+def gdn_fold(p, h_ptrs, conv_state_ptrs, h_out_ptrs, conv_out_ptrs, tape, len_out, B, share,
+             min_len, stream):
+    return load().gdn_fold(ctypes.byref(p), _p(h_ptrs), _p(conv_state_ptrs), _p(h_out_ptrs),
+                           _p(conv_out_ptrs), ctypes.byref(tape), _p(len_out), B, share,
+                           min_len, stream)
+
+
+def kda_fold(p, h_ptrs, conv_state_ptrs, h_out_ptrs, conv_out_ptrs, tape, len_out, B, share,
+             min_len, stream):
+    return load().kda_fold(ctypes.byref(p), _p(h_ptrs), _p(conv_state_ptrs), _p(h_out_ptrs),
+                           _p(conv_out_ptrs), ctypes.byref(tape), _p(len_out), B, share,
+                           min_len, stream)
+
+
+def gdn_verify(target, ld_target, draft, ld_draft, dtype, tokens, num_drafts, u, B, T, V,
+               accepted, next, len, ws, ws_bytes, stream):
+    return load().gdn_verify(_p(target), ld_target, _p(draft), ld_draft, dtype, _p(tokens),
+                             _p(num_drafts), _p(u), B, T, V, _p(accepted), _p(next), _p(len),
+                             _p(ws), ws_bytes, stream)
+
+
+def gdn_verify_workspace_bytes(B, T, V):
+    return int(load().gdn_verify_workspace_bytes(B, T, V))
 
 
 def gdn_chunk_table(cu_seqlens, B, chunk, table, max_entries, count, stream):

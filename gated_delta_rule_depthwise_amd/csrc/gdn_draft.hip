@@ -1,0 +1,751 @@
+// gdn_draft.hip -- drafted tokens on gfx950: T tokens per stream against states that are only
+// read (draft_kernel), and the streams' tapes worked into their states (fold_kernel).
+//
+// With h the state in memory, k_j, d_j the entries of a stream's tape (or its new tokens)
+// and G the running sum of log-gates from h on, the new token t gives
+//   y_t = h^T (e^{G_t} k_t) + sum_{j before t} (k_j . e^{G_t - G_j} k_t) d_j,
+//   d_t = beta_t (v_t - y_t),
+//   o_t = h^T (e^{G_t} q_t) + sum_{j up to t} (k_j . e^{G_t - G_j} q_t) d_j,
+// so the state is read once for all the tokens (and streams) of a workgroup and never
+// written: the whole call moves about half the bytes of one in-place decode step. The
+// products with h, with the tape's keys and with its updates run on fp32 MFMA; the part
+// among the new tokens is a triangular solve of at most 16 steps per column.
+//
+// fold: h_out = diag(e^{G_n}) h + sum_j diag(e^{G_n - G_j}) k_j d_j^T, a rank-n update on
+// fp32 MFMA of a state that is read and written once.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdn.h"
+#include "gdn_internal.h"
+
+namespace gdn {
+
+namespace {
+
+typedef __bf16 bf16;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int THREADS = 256;
+constexpr int WAVES = THREADS / 64;
+
+__device__ __forceinline__ f32x4 load_nt4(const float *p)
+{
+    return __builtin_nontemporal_load((const f32x4 *)p);
+}
+__device__ __forceinline__ f32x4 load4(const float *p) { return *(const f32x4 *)p; }
+__device__ __forceinline__ f32x4 load4(const bf16 *p)
+{
+    const uint2 u = *(const uint2 *)p;
+    return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                 __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u)};
+}
+
+__device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
+
+__device__ __forceinline__ f32x4 mfma4(float a, float b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+// two adjacent channels of a raw row, kept as loaded (the tape takes the same bits)
+template <typename T> struct Pair;
+template <> struct Pair<bf16> {
+    typedef uint32_t raw;
+    static __device__ __forceinline__ float lo(raw r) { return __uint_as_float(r << 16); }
+    static __device__ __forceinline__ float hi(raw r) { return __uint_as_float(r & 0xffff0000u); }
+    static __device__ __forceinline__ raw make(const bf16 *a, const bf16 *b)
+    {
+        return (uint32_t)*(const uint16_t *)a | (uint32_t)*(const uint16_t *)b << 16;
+    }
+};
+template <> struct Pair<float> {
+    typedef float2 raw;
+    static __device__ __forceinline__ float lo(raw r) { return r.x; }
+    static __device__ __forceinline__ float hi(raw r) { return r.y; }
+    static __device__ __forceinline__ raw make(const float *a, const float *b)
+    {
+        return float2{*a, *b};
+    }
+};
+
+__device__ __forceinline__ float silu(float x) { return x / (1.f + __expf(-x)); }
+
+// Sum over groups of N lanes, every lane gets it.
+template <int N> __device__ __forceinline__ float group_sum(float x)
+{
+#pragma unroll
+    for (int m = 1; m < N; m <<= 1)
+        x += __shfl_xor(x, m);
+    return x;
+}
+
+// One workgroup: one state (prefix, head) and a tile of up to TOK tokens of its streams, ns
+// streams of T tokens. Rows of the products are the tokens' keys (rows 0 .. TOK-1) and
+// queries (TOK .. 2*TOK-1).
+template <int DK, int DV, bool KDA, int TOK> struct DraftShape {
+    static constexpr int R = 2 * TOK;          // rows of the products
+    static constexpr int MT = R / 16;          // 16-row MFMA tiles
+    static constexpr int NS = TOK < 8 ? TOK : 8;  // streams per tile, at most
+    static constexpr int CG = DV / 64;         // 64-column groups, one wave (or more) each
+    static constexpr int RS = WAVES / CG;      // waves that share a column group's rows
+    static constexpr int RW = DK / RS;         // rows of h per wave
+    static constexpr int LDK = DK + 4;         // row stride of the key tiles
+    static constexpr int LDS_ = 20;            // row stride of the score tile
+    static constexpr int KS = WAVES / MT;      // channel parts of the score product
+    // LDS, in floats; the partial products Y overlay everything that is dead by then
+    static constexpr int KQ = 0;
+    static constexpr int KT = KQ + R * LDK;                   // 16 tape keys
+    static constexpr int SP = KT + 16 * LDK;                  // partial scores
+    static constexpr int GK = SP + KS * R * LDS_;             // KDA: new tokens' log-gates
+    static constexpr int ET = GK + (KDA ? TOK * DK : 0);      // KDA: e^{tape's total}
+    static constexpr int END1 = ET + (KDA ? NS * DK : 0);
+    static constexpr int Y = 0;
+    static constexpr int END2 = RS * R * DV;
+    static constexpr int VD = END1 > END2 ? END1 : END2;      // v, then d
+    static constexpr int CO = VD + TOK * DV;                  // coefficients among new tokens
+    static constexpr int SM = CO + R * TOK;                   // small: see the kernel
+    static constexpr int TOTAL = SM + 3 * TOK + 16 + 2 * NS;
+    static_assert(TOTAL * 4 <= 65536, "static LDS");
+    static_assert(RW % 16 == 0 && WAVES % MT == 0 && DK % (16 * KS) == 0, "tile map");
+};
+
+template <typename T, int DK, int DV, bool KDA, int K, int TOK>
+__global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int ntile)
+{
+    using S = DraftShape<DK, DV, KDA, TOK>;
+    using P = Pair<T>;
+    constexpr int W = K > 0 ? K - 1 : 0;
+    constexpr int R = S::R, MT = S::MT, NS = S::NS, LDK = S::LDK;
+    __shared__ __align__(16) float sm[S::TOTAL];
+    float *const kq = sm + S::KQ, *const kt = sm + S::KT, *const sp = sm + S::SP;
+    float *const gk = sm + S::GK, *const et = sm + S::ET, *const y = sm + S::Y;
+    float *const vd = sm + S::VD, *const co = sm + S::CO;
+    float *const gam = sm + S::SM;        // [TOK] log-gates through each new token (GDN)
+    float *const bet = gam + TOK;         // [TOK]
+    float *const suf = bet + TOK;         // [16] log-decay after each tape entry (GDN)
+    float *const tot = suf + 16;          // [NS] log-decay of the whole tape (GDN)
+    int *const slen = (int *)(tot + NS);  // [NS] tape lengths, -1: stream left out
+
+    const int H = a.H, Hqk = a.Hqk, Tn = a.T, cap = a.tape.cap;
+    const int tile = blockIdx.x % ntile, ph = blockIdx.x / ntile;
+    const int head = ph % H, pfx = ph / H;
+    const int rep = H / Hqk, hq = head / rep;
+    const bool own_qk = head % rep == 0;  // this workgroup writes the q/k head's tape entries
+    const int nsmax = TOK / Tn < NS ? TOK / Tn : NS;
+    const int s0 = tile * nsmax;
+    const int ns = a.share - s0 < nsmax ? a.share - s0 : nsmax;
+    const int b0 = pfx * a.share + s0, nt = ns * Tn;
+    const int64_t row0 = (int64_t)b0 * Tn;
+    const int64_t cd = 2 * (int64_t)Hqk * DK + (int64_t)H * DV;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int c16 = lane & 15, g4 = lane >> 4;
+    const int cg = wave % S::CG, rs = wave / S::CG;
+
+    // the state's rows of this wave, 64 columns: 4 adjacent columns per lane
+    f32x4 hr[S::RW / 4];
+    {
+        const float *hp = a.h_ptrs[pfx] + (int64_t)head * DK * DV +
+                          (int64_t)(rs * S::RW + 4 * g4) * DV + 64 * cg + 4 * c16;
+#pragma unroll
+        for (int i = 0; i < S::RW / 4; ++i)
+            hr[i] = load_nt4(hp + (int64_t)(16 * (i / 4) + i % 4) * DV);
+    }
+
+    if (tid < ns) {
+        int n = a.tape.len[b0 + tid];
+        if (n < 0 || n > cap - Tn) {
+            n = -1;
+            if (a.dbg && head == 0)
+                atomicOr(a.dbg, GDN_BAD_TAPE);
+        }
+        slen[tid] = n;
+    }
+    if (tid >= 64 && tid < 64 + nt)
+        bet[tid - 64] = a.beta[(row0 + tid - 64) * H + head];
+    __syncthreads();
+
+    // ---- front end: a thread takes two adjacent channels of every token -----------------
+    constexpr int CP = (2 * DK + DV) / 2;
+    static_assert(CP <= THREADS, "front end map");
+    if (tid < CP) {
+        const int c = 2 * tid;
+        const int sec = c < DK ? 0 : c < 2 * DK ? 1 : 2;
+        const int e = sec == 0 ? c : sec == 1 ? c - DK : c - 2 * DK;
+        const T *src = (const T *)(sec == 0 ? a.q : sec == 1 ? a.k : a.v);
+        const int64_t col = sec == 2 ? (int64_t)head * DV + e : (int64_t)hq * DK + e;
+        const int64_t ch = (sec == 0 ? 0 : (int64_t)sec * Hqk * DK) + col;
+        float *dst = sec == 2 ? vd + e : kq + (sec == 0 ? TOK * LDK : 0) + e;
+        const int ldd = sec == 2 ? DV : LDK;
+        typename P::raw raw[TOK], old[TOK][W > 0 ? W : 1];
+        int s = 0, t = 0;
+#pragma unroll
+        for (int tok = 0; tok < TOK; ++tok) {
+            raw[tok] = typename P::raw{};
+            if (tok < nt) {
+                const int n = slen[s];
+                if (n >= 0)
+                    raw[tok] = *(const typename P::raw *)(src + (row0 + tok) * a.ld + col);
+                if (K > 0 && t == 0) {
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        old[tok][i] = typename P::raw{};
+                        const int m = n - W + i;  // the tape entry, or before it the window
+                        if (n >= 0 && m >= 0)
+                            old[tok][i] = *(const typename P::raw *)((const T *)a.tape.raw +
+                                                                      ((int64_t)(b0 + s) * cap + m) * cd + ch);
+                        else if (n >= 0) {
+                            const T *w = (const T *)a.conv_state_ptrs[pfx] + ch * W + W + m;
+                            old[tok][i] = P::make(w, w + W);
+                        }
+                    }
+                }
+                if (++t == Tn)
+                    t = 0, ++s;
+            }
+        }
+        float2 w[K > 0 ? K : 1], win[W > 0 ? W : 1];
+        if constexpr (K > 0) {
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+                w[i] = float2{a.conv_w[ch * K + i], a.conv_w[(ch + 1) * K + i]};
+        }
+        s = 0, t = 0;
+#pragma unroll
+        for (int tok = 0; tok < TOK; ++tok) {
+            float x0 = P::lo(raw[tok]), x1 = P::hi(raw[tok]);
+            if (tok < nt) {
+                const int n = slen[s];
+                if constexpr (K > 0) {
+                    if (t == 0) {
+#pragma unroll
+                        for (int i = 0; i < W; ++i)
+                            win[i] = float2{P::lo(old[tok][i]), P::hi(old[tok][i])};
+                    }
+                    float a0 = w[K - 1].x * x0, a1 = w[K - 1].y * x1;
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        a0 += w[i].x * win[i].x, a1 += w[i].y * win[i].y;
+#pragma unroll
+                    for (int i = 0; i + 1 < W; ++i)
+                        win[i] = win[i + 1];
+                    win[W - 1] = float2{x0, x1};
+                    x0 = silu(a0), x1 = silu(a1);
+                    if (n >= 0 && (sec == 2 || own_qk))
+                        *(typename P::raw *)((T *)a.tape.raw +
+                                             ((int64_t)(b0 + s) * cap + n + t) * cd + ch) = raw[tok];
+                }
+                if (++t == Tn)
+                    t = 0, ++s;
+            }
+            dst[tok * ldd] = x0, dst[tok * ldd + 1] = x1;
+        }
+    }
+    // ---- log-gates of the new tokens, and onto the tape --------------------------------
+    if constexpr (KDA) {
+        for (int i = tid; i < nt * (DK / 4); i += THREADS) {
+            const int tok = i / (DK / 4), c = 4 * (i % (DK / 4)), s = tok / Tn;
+            const f32x4 gv = load4(a.g + ((row0 + tok) * H + head) * DK + c);
+            *(f32x4 *)(gk + tok * DK + c) = gv;
+            if (slen[s] >= 0)
+                *(f32x4 *)(a.tape.g + (((int64_t)(b0 + s) * cap + slen[s] + tok - s * Tn) * H + head) * DK + c) = gv;
+        }
+    } else {
+        if (tid < nt) {
+            const int s = tid / Tn;
+            const float gv = a.g[(row0 + tid) * H + head];
+            gam[tid] = gv;
+            if (slen[s] >= 0)
+                a.tape.g[((int64_t)(b0 + s) * cap + slen[s] + tid - s * Tn) * H + head] = gv;
+        }
+    }
+    __syncthreads();
+
+    // ---- L2 and scale: 16 lanes per row; normalised keys onto the tape ------------------
+#pragma unroll
+    for (int m = tid >> 4; m < R; m += THREADS / 16) {
+        const int tok = m % TOK, l = tid & 15;
+        float *x = kq + m * LDK + 4 * l;
+        f32x4 v[DK / 64];
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < DK / 64; ++i) {
+            v[i] = load4(x + 64 * i);
+            ss += v[i].x * v[i].x + v[i].y * v[i].y + v[i].z * v[i].z + v[i].w * v[i].w;
+        }
+        ss = group_sum<16>(ss);
+        float mul = a.do_l2 ? 1.f / sqrtf(ss + a.eps) : 1.f;
+        if (m >= TOK)
+            mul *= a.scale;
+        const int s = tok / Tn;
+        const bool put = m < TOK && own_qk && tok < nt && slen[s < NS ? s : 0] >= 0;
+#pragma unroll
+        for (int i = 0; i < DK / 64; ++i) {
+            v[i] *= mul;
+            if (tok >= nt)
+                v[i] = zero4();
+            *(f32x4 *)(x + 64 * i) = v[i];
+            if (put)
+                *(f32x4 *)(a.tape.k + (((int64_t)(b0 + s) * cap + slen[s] + tok - s * Tn) * Hqk + hq) * DK +
+                           4 * l + 64 * i) = v[i];
+        }
+    }
+    // running sums of the log-gates within each stream's new tokens
+    if constexpr (KDA) {
+        if (tid < DK) {
+            int t = 0;
+            float sum = 0.f;
+            for (int tok = 0; tok < nt; ++tok) {
+                sum = (t == 0 ? 0.f : sum) + gk[tok * DK + tid];
+                gk[tok * DK + tid] = sum;
+                if (++t == Tn)
+                    t = 0;
+            }
+        }
+    } else if (tid < ns) {
+        float sum = 0.f;
+        for (int t = 0; t < Tn; ++t)
+            gam[tid * Tn + t] = sum += gam[tid * Tn + t];
+    }
+    __syncthreads();
+
+    // ---- coefficients among the new tokens: 16 lanes per pair ----------------------------
+    for (int idx = tid >> 4; idx < R * TOK; idx += THREADS / 16) {
+        const int m = idx / TOK, j = idx % TOK, tok = m % TOK, l = tid & 15;
+        if (tok >= nt || tok / Tn != j / Tn || (m < TOK ? j >= tok : j > tok))
+            continue;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < DK / 64; ++i) {
+            const f32x4 x = load4(kq + m * LDK + 4 * l + 64 * i);
+            f32x4 kj = load4(kq + j * LDK + 4 * l + 64 * i);
+            if constexpr (KDA) {
+                const f32x4 e = load4(gk + tok * DK + 4 * l + 64 * i) - load4(gk + j * DK + 4 * l + 64 * i);
+                kj.x *= __expf(e.x), kj.y *= __expf(e.y), kj.z *= __expf(e.z), kj.w *= __expf(e.w);
+            }
+            sum += x.x * kj.x + x.y * kj.y + x.z * kj.z + x.w * kj.w;
+        }
+        sum = group_sum<16>(sum);
+        if constexpr (!KDA)
+            sum *= __expf(gam[tok] - gam[j]);
+        if (l == 0)
+            co[idx] = sum;
+    }
+    if constexpr (KDA) {  // keys and queries take the decay through their token
+        __syncthreads();
+        for (int i = tid; i < R * (DK / 4); i += THREADS) {
+            const int m = i / (DK / 4), c = 4 * (i % (DK / 4)), tok = m % TOK;
+            if (tok < nt) {
+                const f32x4 e = load4(gk + tok * DK + c);
+                float *x = kq + m * LDK + c;
+                *(f32x4 *)x = load4(x) * f32x4{__expf(e.x), __expf(e.y), __expf(e.z), __expf(e.w)};
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- the tapes: 16 entries at a time, newest first -----------------------------------
+    f32x4 acc[MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[mt][j] = zero4();
+    for (int s = 0; s < ns; ++s) {
+        const int n = slen[s] < 0 ? 0 : slen[s];
+        const int64_t e0 = (int64_t)(b0 + s) * cap;
+        float run = 0.f;  // KDA: thread c's log-decay over the newer entries; GDN: thread 0's
+        f32x4 add[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                add[mt][j] = zero4();
+        for (int eb = (n - 1) / 16 * 16; eb >= 0 && n > 0; eb -= 16) {
+            const int ne = n - eb < 16 ? n - eb : 16;
+            // keys; for KDA with the decay after each entry
+            if constexpr (KDA) {
+                if (tid < DK) {
+                    for (int e = ne - 1; e >= 0; --e) {
+                        kt[e * LDK + tid] = __expf(run);
+                        run += a.tape.g[((e0 + eb + e) * H + head) * DK + tid];
+                    }
+                }
+                __syncthreads();
+            } else if (tid == 0) {
+                for (int e = ne - 1; e >= 0; --e) {
+                    suf[e] = run;
+                    run += a.tape.g[(e0 + eb + e) * H + head];
+                }
+            }
+            for (int i = tid; i < 16 * (DK / 4); i += THREADS) {
+                const int e = i / (DK / 4), c = 4 * (i % (DK / 4));
+                f32x4 kv = zero4();
+                if (e < ne) {
+                    kv = load4(a.tape.k + ((e0 + eb + e) * Hqk + hq) * DK + c);
+                    if constexpr (KDA)
+                        kv *= load4(kt + e * LDK + c);
+                }
+                *(f32x4 *)(kt + e * LDK + c) = kv;
+            }
+            __syncthreads();
+            {  // scores of the rows with the 16 keys; a wave takes a row tile and channels
+                const int mt = wave % MT, part = wave / MT;
+                f32x4 sc = zero4();
+#pragma unroll
+                for (int cc = 0; cc < DK / (16 * S::KS); ++cc) {
+                    const int c = part * (DK / S::KS) + 16 * cc + 4 * g4;
+                    const f32x4 av = load4(kq + (16 * mt + c16) * LDK + c);
+                    const f32x4 bv = load4(kt + c16 * LDK + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sc = mfma4(av[i], bv[i], sc);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    sp[(part * R + 16 * mt + 4 * g4 + r) * S::LDS_ + c16] = sc[r];
+            }
+            __syncthreads();
+            f32x4 av[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const int m = 16 * mt + c16, tok = m % TOK;
+                const bool mine = tok / Tn == s && tok < nt;
+                f32x4 v = zero4();
+#pragma unroll
+                for (int p = 0; p < S::KS; ++p)
+                    v += load4(sp + (p * R + m) * S::LDS_ + 4 * g4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = 4 * g4 + i;
+                    float f = 1.f;
+                    if constexpr (!KDA)
+                        f = __expf(gam[mine ? tok : 0] + suf[e < ne ? e : 0]);
+                    av[mt][i] = mine && e < ne ? v[i] * f : 0.f;
+                }
+            }
+            // the waves of one column group take every RS-th entry
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i % S::RS != rs % 4)
+                    continue;
+                const int e = 4 * g4 + i;
+                f32x4 dv = zero4();
+                if (e < ne)
+                    dv = load4(a.tape.d + ((e0 + eb + e) * H + head) * DV + 64 * cg + 4 * c16);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        add[mt][j] = mfma4(av[mt][i], dv[j], add[mt][j]);
+            }
+            __syncthreads();
+        }
+        if constexpr (KDA) {
+            if (tid < DK)
+                et[s * DK + tid] = __expf(run);
+        } else if (tid == 0)
+            tot[s] = run;
+        // only the stream's own rows: what its entries hold reaches no other stream
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int tok = (16 * mt + 4 * g4 + r) % TOK;
+                if (tok / Tn == s) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[mt][j][r] = add[mt][j][r];
+                }
+            }
+    }
+    __syncthreads();
+
+    // ---- the state ----------------------------------------------------------------------
+    {
+        float f[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int tok = (16 * mt + c16) % TOK;
+            f[mt] = 1.f;
+            if constexpr (!KDA)
+                f[mt] = tok < nt ? __expf(gam[tok] + tot[tok / Tn]) : 0.f;
+        }
+#pragma unroll
+        for (int ss = 0; ss < S::RW / 16; ++ss) {
+            const int c = rs * S::RW + 16 * ss + 4 * g4;
+            f32x4 av[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const int tok = (16 * mt + c16) % TOK;
+                av[mt] = load4(kq + (16 * mt + c16) * LDK + c);
+                if constexpr (KDA)
+                    av[mt] *= tok < nt ? load4(et + (tok / Tn) * DK + c) : zero4();
+                else
+                    av[mt] *= f[mt];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[mt][j] = mfma4(av[mt][i], hr[4 * ss + i][j], acc[mt][j]);
+        }
+    }
+    __syncthreads();  // Y overlays the key tiles
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            *(f32x4 *)(y + (rs * R + 16 * mt + 4 * g4 + r) * DV + 64 * cg + 4 * c16) =
+                f32x4{acc[mt][0][r], acc[mt][1][r], acc[mt][2][r], acc[mt][3][r]};
+    __syncthreads();
+
+    // ---- the new tokens in order, a thread per column ------------------------------------
+    {
+        constexpr int G = THREADS / DV;
+        const int c = tid % DV;
+        for (int s = tid / DV; s < ns; s += G) {
+            if (slen[s] < 0)
+                continue;
+            for (int t = 0; t < Tn; ++t) {
+                const int tok = s * Tn + t;
+                float yk = 0.f, yq = 0.f;
+#pragma unroll
+                for (int p = 0; p < S::RS; ++p) {
+                    yk += y[(p * R + tok) * DV + c];
+                    yq += y[(p * R + TOK + tok) * DV + c];
+                }
+                for (int j = 0; j < t; ++j) {
+                    const float dj = vd[(s * Tn + j) * DV + c];
+                    yk += co[tok * TOK + s * Tn + j] * dj;
+                    yq += co[(TOK + tok) * TOK + s * Tn + j] * dj;
+                }
+                const float d = bet[tok] * (vd[tok * DV + c] - yk);
+                vd[tok * DV + c] = d;
+                a.tape.d[(((int64_t)(b0 + s) * cap + slen[s] + t) * H + head) * DV + c] = d;
+                y[(TOK + tok) * DV + c] = yq + co[(TOK + tok) * TOK + tok] * d;
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- o, through the output gate if asked ---------------------------------------------
+    constexpr int L = DV / 4;
+    for (int tok = tid / L; tok < nt; tok += THREADS / L) {
+        const int l = tid % L;
+        if (slen[tok / Tn] < 0)
+            continue;
+        f32x4 o = load4(y + (TOK + tok) * DV + 4 * l);
+        if (a.z) {
+            const f32x4 z = load4((const T *)a.z + (row0 + tok) * a.ld_z + (int64_t)head * DV + 4 * l);
+            const f32x4 w = load4(a.norm_w + 4 * l);
+            const float ss = group_sum<L>(o.x * o.x + o.y * o.y + o.z * o.z + o.w * o.w);
+            const float inv = 1.f / sqrtf(ss * (1.f / DV) + a.norm_eps);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[i] *= inv * w[i] * silu(z[i]);
+        }
+        *(f32x4 *)(a.o + ((row0 + tok) * H + head) * DV + 4 * l) = o;
+    }
+}
+
+// One workgroup: one stream and head. The state is held in MFMA accumulator layout: lane
+// (g4, c16) has rows 16*rt + 4*g4 + r and 4 adjacent columns of the wave's 64.
+template <typename T, int DK, int DV, bool KDA>
+__global__ void __launch_bounds__(THREADS) fold_kernel(const FoldArgs a)
+{
+    constexpr int CG = DV / 64, RS = WAVES / CG, RW = DK / RS, RT = RW / 16;
+    constexpr int EB = 16;  // tape entries per round
+    __shared__ __align__(16) float sf[KDA ? EB * DK : EB];  // decay after each entry
+    __shared__ __align__(16) float through[KDA ? DK : 1];   // e^{tape's total}
+
+    const int H = a.H, Hqk = a.Hqk, cap = a.tape.cap;
+    const int b = blockIdx.x / H, head = blockIdx.x % H, pfx = b / a.share;
+    const int rep = H / Hqk, hq = head / rep;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int c16 = lane & 15, g4 = lane >> 4;
+    const int cg = wave % CG, rs = wave / CG;
+    const int n = a.tape.len[b];
+    const bool bad = n < 0 || n > cap;
+    const bool on = !bad && n >= a.min_len;
+    if (head == 0 && tid == 0) {
+        if (bad && a.dbg)
+            atomicOr(a.dbg, GDN_BAD_TAPE);
+        if (a.len_out && a.len_out != a.tape.len)
+            a.len_out[b] = on ? 0 : n;
+    }
+    if (!on)
+        return;
+
+    const int64_t hoff = (int64_t)head * DK * DV + (int64_t)(rs * RW + 4 * g4) * DV + 64 * cg + 4 * c16;
+    const float *hp = a.h_ptrs[pfx] + hoff;
+    f32x4 hr[RT][4];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            hr[rt][r] = load_nt4(hp + (int64_t)(16 * rt + r) * DV);
+
+    // the windows after the tape: the last K-1 raw inputs of the channels of this head (those
+    // of a q/k head by its first value head)
+    if (a.K > 0) {
+        const int W = a.K - 1;
+        const int64_t cd = 2 * (int64_t)Hqk * DK + (int64_t)H * DV;
+        const T *in = (const T *)a.conv_state_ptrs[pfx];
+        T *out = (T *)a.conv_out_ptrs[b];
+        for (int c = tid; c < 2 * DK + DV; c += THREADS) {
+            if (c < 2 * DK && head % rep)
+                continue;
+            const int64_t ch = c < DK       ? (int64_t)hq * DK + c
+                               : c < 2 * DK ? (int64_t)(Hqk + hq) * DK + c - DK
+                                            : 2 * (int64_t)Hqk * DK + (int64_t)head * DV + c - 2 * DK;
+            T w[3];
+            for (int i = 0; i < 3; ++i) {
+                const int m = n - W + i;
+                if (i < W)
+                    w[i] = m >= 0 ? ((const T *)a.tape.raw)[((int64_t)b * cap + m) * cd + ch]
+                                  : in[ch * W + W + m];
+            }
+            for (int i = 0; i < 3; ++i)
+                if (i < W)
+                    out[ch * W + i] = w[i];
+        }
+    }
+
+    f32x4 acc[RT][4];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[rt][j] = zero4();
+    const int64_t e0 = (int64_t)b * cap;
+    float run = 0.f;
+    for (int eb = (n - 1) / EB * EB; eb >= 0 && n > 0; eb -= EB) {
+        const int ne = n - eb < EB ? n - eb : EB;
+        __syncthreads();
+        if constexpr (KDA) {
+            if (tid < DK)
+                for (int e = ne - 1; e >= 0; --e) {
+                    sf[e * DK + tid] = __expf(run);
+                    run += a.tape.g[((e0 + eb + e) * H + head) * DK + tid];
+                }
+        } else if (tid == 0) {
+            for (int e = ne - 1; e >= 0; --e) {
+                sf[e] = __expf(run);
+                run += a.tape.g[(e0 + eb + e) * H + head];
+            }
+        }
+        __syncthreads();
+        for (int q = 0; q < EB; q += 4) {
+            const int e = q + g4;
+            f32x4 dv = zero4();
+            float kv[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+                kv[rt] = 0.f;
+            if (e < ne) {
+                dv = load4(a.tape.d + ((e0 + eb + e) * H + head) * DV + 64 * cg + 4 * c16);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const int c = rs * RW + 16 * rt + c16;
+                    kv[rt] = a.tape.k[((e0 + eb + e) * Hqk + hq) * DK + c] * (KDA ? sf[e * DK + c] : sf[e]);
+                }
+            }
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[rt][j] = mfma4(kv[rt], dv[j], acc[rt][j]);
+        }
+    }
+    if (tid < (KDA ? DK : 1))
+        through[tid] = __expf(run);
+    __syncthreads();
+    float *op = a.h_out_ptrs[b] + hoff;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float f = through[KDA ? rs * RW + 16 * rt + 4 * g4 + r : 0];
+            const f32x4 v = hr[rt][r] * f + f32x4{acc[rt][0][r], acc[rt][1][r], acc[rt][2][r], acc[rt][3][r]};
+            __builtin_nontemporal_store(v, (f32x4 *)(op + (int64_t)(16 * rt + r) * DV));
+        }
+}
+
+// tape lengths after a fold that was asked to clear them in place
+__global__ void __launch_bounds__(THREADS) fold_len_kernel(int32_t *len, int32_t B, int32_t cap, int32_t min_len)
+{
+    const int b = blockIdx.x * THREADS + threadIdx.x;
+    if (b < B && len[b] <= cap && len[b] >= min_len)
+        len[b] = 0;
+}
+
+template <typename T, int DK, int DV, bool KDA, int TOK>
+hipError_t draft_k(const DraftArgs &a, hipStream_t s)
+{
+    using S = DraftShape<DK, DV, KDA, TOK>;
+    const int ns = TOK / a.T < S::NS ? TOK / a.T : S::NS;
+    const int ntile = (a.share + ns - 1) / ns;
+    const int64_t grid = (int64_t)(a.B / a.share) * a.H * ntile;
+    if (grid > (int64_t)INT32_MAX)
+        return hipErrorInvalidValue;
+    const dim3 g((unsigned)grid), t(THREADS);
+    switch (a.K) {
+    case 0: hipLaunchKernelGGL((draft_kernel<T, DK, DV, KDA, 0, TOK>), g, t, 0, s, a, ntile); break;
+    case 2: hipLaunchKernelGGL((draft_kernel<T, DK, DV, KDA, 2, TOK>), g, t, 0, s, a, ntile); break;
+    case 3: hipLaunchKernelGGL((draft_kernel<T, DK, DV, KDA, 3, TOK>), g, t, 0, s, a, ntile); break;
+    case 4: hipLaunchKernelGGL((draft_kernel<T, DK, DV, KDA, 4, TOK>), g, t, 0, s, a, ntile); break;
+    default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+template <typename T, int DK, int DV, bool KDA> hipError_t draft_t(const DraftArgs &a, hipStream_t s)
+{
+    return a.T <= 8 ? draft_k<T, DK, DV, KDA, 8>(a, s) : draft_k<T, DK, DV, KDA, 16>(a, s);
+}
+
+template <typename T, int DK, int DV, bool KDA> hipError_t fold_t(const FoldArgs &a, hipStream_t s)
+{
+    hipLaunchKernelGGL((fold_kernel<T, DK, DV, KDA>), dim3((unsigned)((int64_t)a.B * a.H)), dim3(THREADS), 0, s, a);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess)
+        return e;
+    if (a.len_out == a.tape.len)
+        hipLaunchKernelGGL(fold_len_kernel, dim3((unsigned)((a.B + THREADS - 1) / THREADS)), dim3(THREADS), 0, s,
+                           a.tape.len, a.B, a.tape.cap, a.min_len);
+    return hipGetLastError();
+}
+
+// f<T, DK, DV, KDA>(a, s) for the compiled configurations: bf16 (64, 64), (128, 128) and
+// (128, 256), float32 (64, 64) and (64, 128)
+#define GDN_DISPATCH(F, a, s)                                                                   \
+    if (dtype) {                                                                                \
+        if ((a).dk == 128 && (a).dv == 128)                                                     \
+            return kda ? F<bf16, 128, 128, true>(a, s) : F<bf16, 128, 128, false>(a, s);        \
+        if ((a).dk == 128 && (a).dv == 256)                                                     \
+            return kda ? F<bf16, 128, 256, true>(a, s) : F<bf16, 128, 256, false>(a, s);        \
+        if ((a).dk == 64 && (a).dv == 64)                                                       \
+            return kda ? F<bf16, 64, 64, true>(a, s) : F<bf16, 64, 64, false>(a, s);            \
+    } else {                                                                                    \
+        if ((a).dk == 64 && (a).dv == 64)                                                       \
+            return kda ? F<float, 64, 64, true>(a, s) : F<float, 64, 64, false>(a, s);          \
+        if ((a).dk == 64 && (a).dv == 128)                                                      \
+            return kda ? F<float, 64, 128, true>(a, s) : F<float, 64, 128, false>(a, s);        \
+    }                                                                                           \
+    return hipErrorInvalidValue
+
+}  // namespace
+
+hipError_t launch_draft(int dtype, int kda, const DraftArgs &a, hipStream_t s)
+{
+    GDN_DISPATCH(draft_t, a, s);
+}
+
+hipError_t launch_fold(int dtype, int kda, const FoldArgs &a, hipStream_t s)
+{
+    GDN_DISPATCH(fold_t, a, s);
+}
+
+}  // namespace gdn

@@ -172,3 +172,90 @@ class Decode:
         p = self._params(T * sp.cd, zp, T * sp.H * sp.dv)
         return self._call(p, base, base + sp.qk_heads * sp.dk * es,
                           base + 2 * sp.qk_heads * sp.dk * es, g, beta, stream)
+
+
+class Drafts:
+    """Streams with tapes: gdn_draft / kda_draft and gdn_fold / kda_fold on one set of device
+    buffers.
+
+    ``spec`` is an :class:`inputs.Spec` (its heads, dims, dtype, gate, conv and output gate; the
+    lengths are not used). ``share`` consecutive streams read one state. ``h`` is
+    ``[B/share, H, dk, dv]``, ``conv_state`` ``[B/share, cd, K-1]``; the tapes hold ``cap``
+    entries per stream (``k``, ``d``, ``g``, ``raw``) and start empty (``len`` zero).
+    """
+
+    def __init__(self, spec, B_, cap, h, conv_state=None, conv_w=None, share=1, device="cuda",
+                 norm_w=None, fill=0.0, eps=None, scale=None):
+        self.spec, self.B, self.cap, self.share, self.device = spec, B_, cap, share, device
+        td = spec.torch_dtype
+        self.eps = spec.eps if eps is None else eps
+        self.scale = spec.scale if scale is None else scale
+        self.h = h.to(device)
+        self.conv_state = None if conv_state is None else conv_state.to(device)
+        self.conv_w = None if conv_w is None else conv_w.to(device)
+        self.norm_w = None if norm_w is None else norm_w.to(device)
+        gw = (spec.dk,) if spec.gate == "kda" else ()
+        f32 = dict(dtype=torch.float32, device=device)
+        self.k = torch.full((B_, cap, spec.qk_heads, spec.dk), fill, **f32)
+        self.d = torch.full((B_, cap, spec.H, spec.dv), fill, **f32)
+        self.g = torch.full((B_, cap, spec.H) + gw, fill, **f32)
+        self.raw = None if self.conv_w is None else torch.full(
+            (B_, cap, spec.cd), fill, dtype=td, device=device)
+        self.len = torch.zeros(B_, dtype=torch.int32, device=device)
+        self.h_ptrs = self._ptrs(self.h)
+        self.cs_ptrs = None if self.conv_state is None else self._ptrs(self.conv_state)
+
+    def _ptrs(self, t):
+        return torch.tensor([t[i].data_ptr() for i in range(t.shape[0])], dtype=torch.int64,
+                            device=self.device)
+
+    def tape(self):
+        return B.tape(self.k, self.d, self.g, self.raw, self.len, self.cap)
+
+    def params(self, ld=None, z=None, ld_z=None):
+        sp = self.spec
+        return B.params(sp.H, sp.dk, sp.dv, eps=self.eps, scale=self.scale,
+                        dtype=B.GDN_BF16 if sp.dtype == "bf16" else B.GDN_F32,
+                        conv_k=0 if self.conv_w is None else sp.conv_k,
+                        ld_qkv=sp.cd if ld is None else ld, z=z,
+                        norm_w=None if z is None else self.norm_w, ld_z=ld_z,
+                        norm_eps=sp.norm_eps, Hqk=sp.Hqk)
+
+    def draft(self, x, g, beta, o, T, z=None, stream=None) -> int:
+        """T tokens per stream from rows ``x`` [B*T, >= cd] (row stride = its own), gates and
+        betas, into ``o`` [B*T, H, dv]."""
+        sp = self.spec
+        s = torch.cuda.current_stream(self.device).cuda_stream if stream is None else stream
+        es, base = x.element_size(), x.data_ptr()
+        p = self.params(x.stride(0), z, None if z is None else z.stride(0))
+        fn = B.kda_draft if sp.gate == "kda" else B.gdn_draft
+        return fn(p, base, base + sp.qk_heads * sp.dk * es, base + 2 * sp.qk_heads * sp.dk * es,
+                  g, beta, self.h_ptrs, self.cs_ptrs, self.conv_w, self.tape(), o, self.B, T,
+                  self.share, s)
+
+    def fold(self, h_out=None, conv_out=None, len_out=None, min_len=0, stream=None) -> int:
+        """Fold into ``h_out`` / ``conv_out`` (None: in place, share 1); ``len_out`` None:
+        the tapes' own lengths are cleared."""
+        s = torch.cuda.current_stream(self.device).cuda_stream if stream is None else stream
+        hp = self.h_ptrs if h_out is None else self._ptrs(h_out)
+        cp = self.cs_ptrs if conv_out is None else self._ptrs(conv_out)
+        self._kept = (hp, cp)  # the call reads them after it returns
+        fn = B.kda_fold if self.spec.gate == "kda" else B.gdn_fold
+        return fn(self.params(), self.h_ptrs, self.cs_ptrs, hp, cp, self.tape(),
+                  self.len if len_out is None else len_out, self.B, self.share, min_len, s)
+
+
+def verify(target, tokens, u, draft=None, num=None, len=None, stream=None):
+    """gdn_verify on device tensors: target [B, T+1, V], draft [B, T, V] or None, tokens
+    [B, T] int32, u [B, T+1]. Returns (status, accepted [B], next [B])."""
+    Bn, T1, V = target.shape
+    dev = target.device
+    s = torch.cuda.current_stream(dev).cuda_stream if stream is None else stream
+    n = B.gdn_verify_workspace_bytes(Bn, T1 - 1, V)
+    ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+    acc = torch.full((Bn,), -7, dtype=torch.int32, device=dev)
+    nxt = torch.full((Bn,), -7, dtype=torch.int32, device=dev)
+    rc = B.gdn_verify(target, target.stride(1), draft, V if draft is None else draft.stride(1),
+                      B.GDN_BF16 if target.dtype == torch.bfloat16 else B.GDN_F32, tokens, num, u,
+                      Bn, T1 - 1, V, acc, nxt, len, ws, n, s)
+    return rc, acc, nxt

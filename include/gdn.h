@@ -1,6 +1,7 @@
 /*
  * gdn.h -- C ABI of libgdn: the chunked gated-delta-rule prefill (GDN and KDA) on MI355X,
- * its single-token decode step, and the gated RMSNorm of the output.
+ * its single-token decode step, the gated RMSNorm of the output, and the steps on drafted
+ * tokens (draft, verify, fold), which leave the states as they are until tokens count.
  *
  * The operation (pages "split_prefill.rs" -- prefill_gdn_full, prefill_gdn_full_batched,
  * prefill_gdn_full_batched_fla_varlen -- and "metrale_model_arch/glm5next_kda/prefill.rs"
@@ -256,6 +257,121 @@ int kda_decode(const gdn_params *p, const void *q, const void *k, const void *v,
                void *stream);
 
 /*
+ * Tokens that are not yet part of a state.
+ *
+ * gdn_draft runs T tokens per stream against states that it only reads, and appends what the
+ * tokens would add to them to the streams' tapes; gdn_verify decides how many of the drafted
+ * tokens count, and moves the tapes' lengths on; gdn_fold works the tapes into the states.
+ * Going back to an earlier token is a smaller length: no copy of a state is ever needed, and
+ * streams that continue one prompt (share > 1) read its state once for all of them.
+ *
+ * The tape of stream b holds entries 0 .. len[b]-1, the tokens taken since its state was
+ * written, oldest first. With k_i, g_i and d_i those of entry i, the state after entry n is
+ *     h_n = diag(e^(g_0 + .. + g_n)) h + sum_{i<=n} diag(e^(g_{i+1} + .. + g_n)) k_i d_i^T,
+ *     d_i = beta_i (v_i - h_{i-1}^T diag(alpha_i) k_i),
+ * which is the recurrence of step 3 above. All pointers are DEVICE pointers, the struct is
+ * a host one, read during the call only. The tape of stream b starts at entry b*cap.
+ */
+typedef struct gdn_tape {
+    float *k;     /* [B][cap][Hqk][dk]  keys after the front end and L2; 16-byte aligned    */
+    float *d;     /* [B][cap][H][dv]    updates; 16-byte aligned                            */
+    float *g;     /* [B][cap][H] log-gates (KDA: [B][cap][H][dk], 16-byte aligned)          */
+    void *raw;    /* [B][cap][cd] raw rows [q | k | v] in dtype, 16-byte aligned (NULL iff
+                     conv_k == 0): the conv reads the last conv_k-1 of them                 */
+    int32_t *len; /* [B] entries in use                                                     */
+    int32_t cap;  /* entries per stream, >= 1                                               */
+} gdn_tape;
+
+/*
+ * T new tokens per stream (1 <= T <= GDN_DRAFT_MAX_T) after the entries of the stream's tape.
+ * Row b*T + t is token t of stream b; rows, gates, front end, L2, scale, shared q/k heads and
+ * the output gate are those of gdn_prefill_batched with t_per_stream = T, and o is what that
+ * call writes when it starts from the state after the tape. The states, the carried windows
+ * and tape->len stay as they are; the T tokens are written to entries len[b] .. len[b]+T-1
+ * (k, g, d, raw), and count once the caller (or gdn_verify) raises len[b].
+ *   h_ptrs          device array of B/share device pointers, each to a [H][dk][dv] float
+ *                   state, 16-byte aligned; stream b reads h_ptrs[b / share].
+ *   conv_state_ptrs device array of B/share device pointers to [cd][conv_k-1] windows: the
+ *                   raw inputs before the tape's first entry (NULL iff conv_k == 0).
+ *   share           consecutive streams per state; B must be a multiple of it. The state is
+ *                   read once for as many of its streams' tokens as a workgroup holds.
+ *   o               [B*T][H][dv] float32, out (16-byte aligned).
+ * A stream with len[b] < 0 or len[b] + T > cap is left out: none of its rows of o nor entries
+ * are written (with gdn_debug_validate on, GDN_BAD_TAPE is set); the others are not affected.
+ * Tokens see only themselves and what came before: NaN in a row, a stream or in entries past
+ * len[b] reaches nothing else. Arithmetic is fp32 throughout. KDA gates must be a decay.
+ * (dk, dv) as for gdn_decode. No workspace; one kernel, in GDN_PROF_RECUR when profiling.
+ */
+#define GDN_DRAFT_MAX_T 16
+int gdn_draft(const gdn_params *p, const void *q, const void *k, const void *v,
+              const float *g, const float *beta, const float *const *h_ptrs,
+              const void *const *conv_state_ptrs, const float *conv_w, const gdn_tape *tape,
+              void *o, int32_t B, int32_t T, int32_t share, void *stream);
+int kda_draft(const gdn_params *p, const void *q, const void *k, const void *v,
+              const float *g, const float *beta, const float *const *h_ptrs,
+              const void *const *conv_state_ptrs, const float *conv_w, const gdn_tape *tape,
+              void *o, int32_t B, int32_t T, int32_t share, void *stream);
+
+/*
+ * The state after the last entry of a stream's tape, and the window after it, for every
+ * stream with len[b] >= min_len (min_len >= 0; a stream with an empty tape gets a copy).
+ * The other streams' outputs are left as they were.
+ *   h_ptrs, conv_state_ptrs  as for gdn_draft, read.
+ *   h_out_ptrs      device array of B device pointers to the [H][dk][dv] states written,
+ *                   16-byte aligned. With share == 1 it may be h_ptrs (in place); with
+ *                   share > 1 no output may be a state that other streams still read. The B
+ *                   states must not overlap.
+ *   conv_out_ptrs   likewise for the windows (NULL iff conv_k == 0); in place when it holds
+ *                   the same pointers as conv_state_ptrs and share == 1.
+ *   len_out         NULL, or [B]: 0 for the streams that were folded, len[b] for the others.
+ *                   It may be tape->len itself (a second small launch then clears the
+ *                   lengths); otherwise it must not overlap it.
+ * A stream with len[b] < 0 or len[b] > cap is left out as in gdn_draft (len_out[b] = len[b]).
+ * p: dtype, H, Hqk, dk, dv, conv_k are used; z is ignored.
+ */
+int gdn_fold(const gdn_params *p, const float *const *h_ptrs,
+             const void *const *conv_state_ptrs, float *const *h_out_ptrs,
+             void *const *conv_out_ptrs, const gdn_tape *tape, int32_t *len_out, int32_t B,
+             int32_t share, int32_t min_len, void *stream);
+int kda_fold(const gdn_params *p, const float *const *h_ptrs,
+             const void *const *conv_state_ptrs, float *const *h_out_ptrs,
+             void *const *conv_out_ptrs, const gdn_tape *tape, int32_t *len_out, int32_t B,
+             int32_t share, int32_t min_len, void *stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from given random
+ * numbers (speculative sampling: the tokens kept are distributed as the target's).
+ * Stream b has n_b drafts, each drawn from the proposal's probabilities q_t:
+ *     draft t is accepted while u[b][t] * q_t(token_t) < p_t(token_t), in order from t = 0;
+ *     a = the number of drafts accepted before the first that is not;
+ *     r = max(p_a - q_a, 0) where a < n_b, p_a where all were accepted (r = p_a too where
+ *     max(p_a - q_a, 0) is zero everywhere);
+ *     next = the smallest token v with r_0 + .. + r_v > u[b][T] * (r_0 + .. + r_{V-1}).
+ *   target     probabilities p_t, row b*(T+1) + t at target + (b*(T+1) + t)*ld_target
+ *              elements, t = 0 .. T (row n_b follows the last draft), V each, in dtype.
+ *   draft      probabilities q_t, row b*T + t at draft + (b*T + t)*ld_draft; NULL: the
+ *              drafts were not drawn at random, q_t is 1 at token_t and 0 elsewhere.
+ *   dtype      GDN_F32 or GDN_BF16; rows need no alignment beyond their element's.
+ *   tokens     [B][T] int32; a token outside 0 .. V-1 is not accepted (and counts as having
+ *              no probability). NULL only with T == 0.
+ *   num_drafts [B] int32, n_b, clamped to 0 .. T; NULL: T for every stream.
+ *   u          [B][T+1] float in [0, 1).
+ *   accepted   [B] int32, out: a.       next: [B] int32, out (-1: no positive probability).
+ *   len        NULL, or [B] int32 in/out, such as a gdn_tape's len: len[b] += a + 1, the
+ *              accepted drafts and the token before them (a gdn_draft call over the T+1 rows
+ *              of that token and its drafts gave the target's T+1 rows).
+ *   ws         >= gdn_verify_workspace_bytes(B, T, V), 16-byte aligned.
+ * 0 <= T <= 1024, V >= 1, ld >= V. Sums are held in float64; weights that are negative or NaN
+ * count as zero. Only rows a of the probabilities are read whole. Two launches.
+ */
+int gdn_verify(const void *target, int64_t ld_target, const void *draft, int64_t ld_draft,
+               int32_t dtype, const int32_t *tokens, const int32_t *num_drafts,
+               const float *u, int32_t B, int32_t T, int32_t V, int32_t *accepted,
+               int32_t *next, int32_t *len, void *ws, size_t ws_bytes, void *stream);
+/* Bytes of workspace of a gdn_verify call; 0 for invalid arguments. */
+size_t gdn_verify_workspace_bytes(int32_t B, int32_t T, int32_t V);
+
+/*
  * Per-chunk work table of a varlen call (the bookkeeping of
  * prefill_gdn_full_batched_fla_varlen: total_nt = sum_b ceil(len_b/chunk) chunks,
  * max_num_chunks = max_b ceil(len_b/chunk)). Writes, on `stream`, table[4*i .. 4*i+3] =
@@ -368,6 +484,8 @@ int gdn_segment_plan(const gdn_params *p, int32_t kind, int32_t B, int64_t t_per
 #define GDN_BAD_CU_TOTAL 4   /* cu_seqlens[B] != total_tokens                          */
 #define GDN_BAD_CU_MAXLEN 8  /* a stream longer than max_seqlen                        */
 #define GDN_BAD_KDA_GATE 16  /* a per-key-channel log-gate above 0 or NaN, in a real row */
+#define GDN_BAD_TAPE 32      /* gdn_draft / gdn_fold: a tape length out of range (the stream
+                                was left out; the call's other streams ran)              */
 int gdn_debug_validate(int32_t *status);
 
 /*
