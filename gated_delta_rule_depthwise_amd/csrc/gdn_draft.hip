@@ -69,13 +69,46 @@ template <> struct Pair<float> {
     }
 };
 
-__device__ __forceinline__ float silu(float x) { return x / (1.f + __expf(-x)); }
+__device__ __forceinline__ float silu(float x)
+{
+    return x * __builtin_amdgcn_rcpf(1.f + __expf(-x));
+}
 
-// Sum over groups of N lanes, every lane gets it.
+// Cross-lane moves within a row of 16 lanes (DPP: an operand modifier, no LDS round trip). A
+// lane whose source lies outside its row gets 0.
+template <int CTRL> __device__ __forceinline__ float dpp(float x)
+{
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+constexpr int DPP_SHR = 0x110;  // + n: from the lane n below
+
+// Sum over a row of 16 lanes; every lane gets it.
+__device__ __forceinline__ float row_sum(float x)
+{
+    x += dpp<0xb1>(x);   // quad_perm 1,0,3,2
+    x += dpp<0x4e>(x);   // quad_perm 2,3,0,1
+    x += dpp<0x141>(x);  // mirrored half row
+    x += dpp<0x140>(x);  // mirrored row
+    return x;
+}
+
+// Sum over the lanes 0 .. l of a row, at lane l.
+__device__ __forceinline__ float row_scan(float x)
+{
+    x += dpp<DPP_SHR + 1>(x);
+    x += dpp<DPP_SHR + 2>(x);
+    x += dpp<DPP_SHR + 4>(x);
+    x += dpp<DPP_SHR + 8>(x);
+    return x;
+}
+
+// Sum over groups of N lanes (16, 32 or 64), every lane gets it.
 template <int N> __device__ __forceinline__ float group_sum(float x)
 {
+    x = row_sum(x);
 #pragma unroll
-    for (int m = 1; m < N; m <<= 1)
+    for (int m = 16; m < N; m <<= 1)
         x += __shfl_xor(x, m);
     return x;
 }
@@ -90,24 +123,25 @@ template <int DK, int DV, bool KDA, int TOK> struct DraftShape {
     static constexpr int CG = DV / 64;         // 64-column groups, one wave (or more) each
     static constexpr int RS = WAVES / CG;      // waves that share a column group's rows
     static constexpr int RW = DK / RS;         // rows of h per wave
-    static constexpr int LDK = DK + 4;         // row stride of the key tiles
-    static constexpr int LDS_ = 20;            // row stride of the score tile
-    static constexpr int KS = WAVES / MT;      // channel parts of the score product
+    static constexpr int LDK = DK + 4;         // row stride of the key tile
+    static constexpr int LDS_ = 20;            // row stride of the score tiles
+    static constexpr int G = THREADS / DV;     // threads per column
+    static_assert(G == RS, "a part of Y per thread of a column");
     // LDS, in floats; the partial products Y overlay everything that is dead by then
     static constexpr int KQ = 0;
-    static constexpr int KT = KQ + R * LDK;                   // 16 tape keys
-    static constexpr int SP = KT + 16 * LDK;                  // partial scores
-    static constexpr int GK = SP + KS * R * LDS_;             // KDA: new tokens' log-gates
-    static constexpr int ET = GK + (KDA ? TOK * DK : 0);      // KDA: e^{tape's total}
-    static constexpr int END1 = ET + (KDA ? NS * DK : 0);
+    static constexpr int SP = KQ + R * LDK;                   // scores of a block per wave
+    static constexpr int BT = SP + WAVES * R * LDS_;          // log-decay over a wave's block
+    static constexpr int GK = BT + WAVES * (KDA ? DK : 1);    // KDA: new tokens' log-gates
+    static constexpr int END1 = GK + (KDA ? TOK * DK : 0);
     static constexpr int Y = 0;
     static constexpr int END2 = RS * R * DV;
-    static constexpr int VD = END1 > END2 ? END1 : END2;      // v, then d
+    static constexpr int RUN = END1 > END2 ? END1 : END2;     // log-decay over a tape's newer blocks
+    static constexpr int VD = RUN + NS * (KDA ? DK : 1);      // v
     static constexpr int CO = VD + TOK * DV;                  // coefficients among new tokens
     static constexpr int SM = CO + R * TOK;                   // small: see the kernel
-    static constexpr int TOTAL = SM + 3 * TOK + 16 + 2 * NS;
+    static constexpr int TOTAL = SM + 2 * TOK + NS;
     static_assert(TOTAL * 4 <= 65536, "static LDS");
-    static_assert(RW % 16 == 0 && WAVES % MT == 0 && DK % (16 * KS) == 0, "tile map");
+    static_assert(RW % 16 == 0 && DK % 16 == 0, "tile map");
 };
 
 template <typename T, int DK, int DV, bool KDA, int K, int TOK>
@@ -116,16 +150,14 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
     using S = DraftShape<DK, DV, KDA, TOK>;
     using P = Pair<T>;
     constexpr int W = K > 0 ? K - 1 : 0;
-    constexpr int R = S::R, MT = S::MT, NS = S::NS, LDK = S::LDK;
+    constexpr int R = S::R, MT = S::MT, NS = S::NS, LDK = S::LDK, G = S::G;
     __shared__ __align__(16) float sm[S::TOTAL];
-    float *const kq = sm + S::KQ, *const kt = sm + S::KT, *const sp = sm + S::SP;
-    float *const gk = sm + S::GK, *const et = sm + S::ET, *const y = sm + S::Y;
+    float *const kq = sm + S::KQ, *const sp = sm + S::SP, *const bt = sm + S::BT;
+    float *const gk = sm + S::GK, *const y = sm + S::Y, *const run = sm + S::RUN;
     float *const vd = sm + S::VD, *const co = sm + S::CO;
     float *const gam = sm + S::SM;        // [TOK] log-gates through each new token (GDN)
     float *const bet = gam + TOK;         // [TOK]
-    float *const suf = bet + TOK;         // [16] log-decay after each tape entry (GDN)
-    float *const tot = suf + 16;          // [NS] log-decay of the whole tape (GDN)
-    int *const slen = (int *)(tot + NS);  // [NS] tape lengths, -1: stream left out
+    int *const slen = (int *)(bet + TOK); // [NS] tape lengths, -1: stream left out
 
     const int H = a.H, Hqk = a.Hqk, Tn = a.T, cap = a.tape.cap;
     const int tile = blockIdx.x % ntile, ph = blockIdx.x / ntile;
@@ -138,34 +170,25 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
     const int b0 = pfx * a.share + s0, nt = ns * Tn;
     const int64_t row0 = (int64_t)b0 * Tn;
     const int64_t cd = 2 * (int64_t)Hqk * DK + (int64_t)H * DV;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c16 = lane & 15, g4 = lane >> 4;
     const int cg = wave % S::CG, rs = wave / S::CG;
 
-    // the state's rows of this wave, 64 columns: 4 adjacent columns per lane
-    f32x4 hr[S::RW / 4];
-    {
-        const float *hp = a.h_ptrs[pfx] + (int64_t)head * DK * DV +
-                          (int64_t)(rs * S::RW + 4 * g4) * DV + 64 * cg + 4 * c16;
-#pragma unroll
-        for (int i = 0; i < S::RW / 4; ++i)
-            hr[i] = load_nt4(hp + (int64_t)(16 * (i / 4) + i % 4) * DV);
-    }
-
+    // a stream's tape length, -1 where the stream is left out
+    const auto tape_len = [&](int s) {
+        const int n = a.tape.len[b0 + s];
+        return n < 0 || n > cap - Tn ? -1 : n;
+    };
     if (tid < ns) {
-        int n = a.tape.len[b0 + tid];
-        if (n < 0 || n > cap - Tn) {
-            n = -1;
-            if (a.dbg && head == 0)
-                atomicOr(a.dbg, GDN_BAD_TAPE);
-        }
+        const int n = tape_len(tid);
+        if (n < 0 && a.dbg && head == 0)
+            atomicOr(a.dbg, GDN_BAD_TAPE);
         slen[tid] = n;
     }
-    if (tid >= 64 && tid < 64 + nt)
-        bet[tid - 64] = a.beta[(row0 + tid - 64) * H + head];
-    __syncthreads();
 
-    // ---- front end: a thread takes two adjacent channels of every token -----------------
+    // ---- front end: a thread takes two adjacent channels of every token; all its loads go
+    // out together -------------------------------------------------------------------------
     constexpr int CP = (2 * DK + DV) / 2;
     static_assert(CP <= THREADS, "front end map");
     if (tid < CP) {
@@ -178,44 +201,48 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
         float *dst = sec == 2 ? vd + e : kq + (sec == 0 ? TOK * LDK : 0) + e;
         const int ldd = sec == 2 ? DV : LDK;
         typename P::raw raw[TOK], old[TOK][W > 0 ? W : 1];
-        int s = 0, t = 0;
 #pragma unroll
         for (int tok = 0; tok < TOK; ++tok) {
             raw[tok] = typename P::raw{};
-            if (tok < nt) {
-                const int n = slen[s];
-                if (n >= 0)
-                    raw[tok] = *(const typename P::raw *)(src + (row0 + tok) * a.ld + col);
-                if (K > 0 && t == 0) {
-#pragma unroll
-                    for (int i = 0; i < W; ++i) {
-                        old[tok][i] = typename P::raw{};
-                        const int m = n - W + i;  // the tape entry, or before it the window
-                        if (n >= 0 && m >= 0)
-                            old[tok][i] = *(const typename P::raw *)((const T *)a.tape.raw +
-                                                                      ((int64_t)(b0 + s) * cap + m) * cd + ch);
-                        else if (n >= 0) {
-                            const T *w = (const T *)a.conv_state_ptrs[pfx] + ch * W + W + m;
-                            old[tok][i] = P::make(w, w + W);
-                        }
-                    }
-                }
-                if (++t == Tn)
-                    t = 0, ++s;
-            }
+            if (tok < nt)
+                raw[tok] = *(const typename P::raw *)(src + (row0 + tok) * a.ld + col);
         }
         float2 w[K > 0 ? K : 1], win[W > 0 ? W : 1];
         if constexpr (K > 0) {
 #pragma unroll
             for (int i = 0; i < K; ++i)
                 w[i] = float2{a.conv_w[ch * K + i], a.conv_w[(ch + 1) * K + i]};
+            int s = 0, t = 0;
+#pragma unroll
+            for (int tok = 0; tok < TOK; ++tok) {
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    old[tok][i] = typename P::raw{};
+                if (tok < nt) {
+                    if (t == 0) {
+                        const int n = tape_len(s);
+#pragma unroll
+                        for (int i = 0; i < W; ++i) {
+                            const int m = n - W + i;  // the tape entry, or before it the window
+                            if (n >= 0 && m >= 0)
+                                old[tok][i] = *(const typename P::raw *)((const T *)a.tape.raw +
+                                                                          ((int64_t)(b0 + s) * cap + m) * cd + ch);
+                            else if (n >= 0) {
+                                const T *ws = (const T *)a.conv_state_ptrs[pfx] + ch * W + W + m;
+                                old[tok][i] = P::make(ws, ws + W);
+                            }
+                        }
+                    }
+                    if (++t == Tn)
+                        t = 0, ++s;
+                }
+            }
         }
-        s = 0, t = 0;
+        int s = 0, t = 0;
 #pragma unroll
         for (int tok = 0; tok < TOK; ++tok) {
             float x0 = P::lo(raw[tok]), x1 = P::hi(raw[tok]);
             if (tok < nt) {
-                const int n = slen[s];
                 if constexpr (K > 0) {
                     if (t == 0) {
 #pragma unroll
@@ -231,6 +258,7 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
                         win[i] = win[i + 1];
                     win[W - 1] = float2{x0, x1};
                     x0 = silu(a0), x1 = silu(a1);
+                    const int n = tape_len(s);
                     if (n >= 0 && (sec == 2 || own_qk))
                         *(typename P::raw *)((T *)a.tape.raw +
                                              ((int64_t)(b0 + s) * cap + n + t) * cd + ch) = raw[tok];
@@ -241,27 +269,24 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
             dst[tok * ldd] = x0, dst[tok * ldd + 1] = x1;
         }
     }
-    // ---- log-gates of the new tokens, and onto the tape --------------------------------
+    // ---- log-gates and betas of the new tokens ---------------------------------------------
     if constexpr (KDA) {
         for (int i = tid; i < nt * (DK / 4); i += THREADS) {
-            const int tok = i / (DK / 4), c = 4 * (i % (DK / 4)), s = tok / Tn;
-            const f32x4 gv = load4(a.g + ((row0 + tok) * H + head) * DK + c);
-            *(f32x4 *)(gk + tok * DK + c) = gv;
-            if (slen[s] >= 0)
-                *(f32x4 *)(a.tape.g + (((int64_t)(b0 + s) * cap + slen[s] + tok - s * Tn) * H + head) * DK + c) = gv;
-        }
-    } else {
-        if (tid < nt) {
-            const int s = tid / Tn;
-            const float gv = a.g[(row0 + tid) * H + head];
-            gam[tid] = gv;
-            if (slen[s] >= 0)
-                a.tape.g[((int64_t)(b0 + s) * cap + slen[s] + tid - s * Tn) * H + head] = gv;
+            const int tok = i / (DK / 4), c = 4 * (i % (DK / 4));
+            *(f32x4 *)(gk + tok * DK + c) = load4(a.g + ((row0 + tok) * H + head) * DK + c);
         }
     }
+    if (tid >= THREADS - TOK && tid < THREADS - TOK + nt) {
+        const int tok = tid - (THREADS - TOK);
+        bet[tok] = a.beta[(row0 + tok) * H + head];
+        if constexpr (!KDA)
+            gam[tok] = a.g[(row0 + tok) * H + head];
+    }
+    for (int i = tid; i < NS * (KDA ? DK : 1); i += THREADS)
+        run[i] = 0.f;
     __syncthreads();
 
-    // ---- L2 and scale: 16 lanes per row; normalised keys onto the tape ------------------
+    // ---- L2 and scale: 16 lanes per row; the new entries' keys and log-gates ----------------
 #pragma unroll
     for (int m = tid >> 4; m < R; m += THREADS / 16) {
         const int tok = m % TOK, l = tid & 15;
@@ -273,8 +298,8 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
             v[i] = load4(x + 64 * i);
             ss += v[i].x * v[i].x + v[i].y * v[i].y + v[i].z * v[i].z + v[i].w * v[i].w;
         }
-        ss = group_sum<16>(ss);
-        float mul = a.do_l2 ? 1.f / sqrtf(ss + a.eps) : 1.f;
+        ss = row_sum(ss);
+        float mul = a.do_l2 ? __builtin_amdgcn_rsqf(ss + a.eps) : 1.f;
         if (m >= TOK)
             mul *= a.scale;
         const int s = tok / Tn;
@@ -293,19 +318,26 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
     // running sums of the log-gates within each stream's new tokens
     if constexpr (KDA) {
         if (tid < DK) {
-            int t = 0;
+            int s = 0, t = 0;
             float sum = 0.f;
             for (int tok = 0; tok < nt; ++tok) {
-                sum = (t == 0 ? 0.f : sum) + gk[tok * DK + tid];
+                const float gv = gk[tok * DK + tid];
+                if (slen[s] >= 0)
+                    a.tape.g[(((int64_t)(b0 + s) * cap + slen[s] + t) * H + head) * DK + tid] = gv;
+                sum = (t == 0 ? 0.f : sum) + gv;
                 gk[tok * DK + tid] = sum;
                 if (++t == Tn)
-                    t = 0;
+                    t = 0, ++s;
             }
         }
     } else if (tid < ns) {
         float sum = 0.f;
-        for (int t = 0; t < Tn; ++t)
-            gam[tid * Tn + t] = sum += gam[tid * Tn + t];
+        for (int t = 0; t < Tn; ++t) {
+            const float gv = gam[tid * Tn + t];
+            if (slen[tid] >= 0)
+                a.tape.g[((int64_t)(b0 + tid) * cap + slen[tid] + t) * H + head] = gv;
+            gam[tid * Tn + t] = sum += gv;
+        }
     }
     __syncthreads();
 
@@ -325,7 +357,7 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
             }
             sum += x.x * kj.x + x.y * kj.y + x.z * kj.z + x.w * kj.w;
         }
-        sum = group_sum<16>(sum);
+        sum = row_sum(sum);
         if constexpr (!KDA)
             sum *= __expf(gam[tok] - gam[j]);
         if (l == 0)
@@ -341,135 +373,174 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
                 *(f32x4 *)x = load4(x) * f32x4{__expf(e.x), __expf(e.y), __expf(e.z), __expf(e.w)};
             }
         }
+        __syncthreads();
     }
-    __syncthreads();
 
-    // ---- the tapes: 16 entries at a time, newest first -----------------------------------
-    f32x4 acc[MT][4];
+    // ---- the tapes, in blocks of 16 entries of one stream, newest first: each round every
+    // wave scores one block against all rows; then a thread per column adds the block's
+    // updates to the rows of the block's own stream (so what a tape holds reaches no other
+    // stream, be it NaN) ---------------------------------------------------------------------
+    const int col = tid % DV, grp = tid / DV;
+    float hist[R];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int m = 0; m < R; ++m)
+        hist[m] = 0.f;
+    int nblk = 0;
+    for (int s = 0; s < ns; ++s)
+        nblk += slen[s] > 0 ? (slen[s] + 15) >> 4 : 0;
+    nblk = __builtin_amdgcn_readfirstlane(nblk);
+    // stream of a block, and one past its newest entry
+    const auto block_at = [&](int blk, int &s, int &hi) {
+        s = 0;
+        for (; s < ns; ++s) {
+            const int n = __builtin_amdgcn_readfirstlane(slen[s]);
+            const int nb = n > 0 ? (n + 15) >> 4 : 0;
+            if (blk < nb) {
+                hi = n - 16 * blk;
+                return;
+            }
+            blk -= nb;
+        }
+    };
+    for (int blk0 = 0; blk0 < nblk; blk0 += WAVES) {
+        int s = 0, hi = 1;
+        const bool act = blk0 + wave < nblk;
+        f32x4 kf[DK / 16], ge[KDA ? DK / 16 : 1];
+        float gs = 0.f;
+        if (act) {
+            block_at(blk0 + wave, s, hi);
+            const int e = hi - 1 - c16;  // lane c16: the c16-th newest entry of the block
+            const int64_t at = (int64_t)(b0 + s) * cap + (e > 0 ? e : 0);
+            const float *kp = a.tape.k + (at * Hqk + hq) * DK + 4 * g4;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc[mt][j] = zero4();
-    for (int s = 0; s < ns; ++s) {
-        const int n = slen[s] < 0 ? 0 : slen[s];
-        const int64_t e0 = (int64_t)(b0 + s) * cap;
-        float run = 0.f;  // KDA: thread c's log-decay over the newer entries; GDN: thread 0's
-        f32x4 add[MT][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                add[mt][j] = zero4();
-        for (int eb = (n - 1) / 16 * 16; eb >= 0 && n > 0; eb -= 16) {
-            const int ne = n - eb < 16 ? n - eb : 16;
-            // keys; for KDA with the decay after each entry
+            for (int i = 0; i < DK / 16; ++i)
+                kf[i] = load4(kp + 16 * i);
+            // log-decay over the block's newer entries, and over the whole block
             if constexpr (KDA) {
-                if (tid < DK) {
-                    for (int e = ne - 1; e >= 0; --e) {
-                        kt[e * LDK + tid] = __expf(run);
-                        run += a.tape.g[((e0 + eb + e) * H + head) * DK + tid];
-                    }
+                const float *gp = a.tape.g + (at * H + head) * DK + 4 * g4;
+#pragma unroll
+                for (int i = 0; i < DK / 16; ++i) {
+                    ge[i] = e >= 0 ? load4(gp + 16 * i) : zero4();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        ge[i][j] = row_scan(ge[i][j]);
+                    if (c16 == 15)
+                        *(f32x4 *)(bt + wave * DK + 16 * i + 4 * g4) = ge[i];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        ge[i][j] = dpp<DPP_SHR + 1>(ge[i][j]);
                 }
-                __syncthreads();
-            } else if (tid == 0) {
-                for (int e = ne - 1; e >= 0; --e) {
-                    suf[e] = run;
-                    run += a.tape.g[(e0 + eb + e) * H + head];
+            } else {
+                gs = row_scan(e >= 0 ? a.tape.g[at * H + head] : 0.f);
+                if (lane == 15)
+                    bt[wave] = gs;
+                gs = dpp<DPP_SHR + 1>(gs);
+            }
+        }
+        __syncthreads();
+        if (act) {
+            // the blocks of this round before this wave's that are of its stream: the last
+            // (hi's distance from the tape's end tells how many) of the waves below
+            int newer = (__builtin_amdgcn_readfirstlane(slen[s]) - hi) >> 4;
+            newer = newer < wave ? newer : wave;
+            f32x4 sc[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                sc[mt] = zero4();
+            if constexpr (!KDA) {
+                gs += run[s];
+                for (int w = wave - newer; w < wave; ++w)
+                    gs += bt[w];
+            }
+#pragma unroll
+            for (int i = 0; i < DK / 16; ++i) {
+                if constexpr (KDA) {
+                    f32x4 x = ge[i] + load4(run + s * DK + 16 * i + 4 * g4);
+                    for (int w = wave - newer; w < wave; ++w)
+                        x += load4(bt + w * DK + 16 * i + 4 * g4);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        kf[i][j] *= __expf(x[j]);
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const f32x4 av = load4(kq + (16 * mt + c16) * LDK + 16 * i + 4 * g4);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        sc[mt] = mfma4(av[j], kf[i][j], sc[mt]);
                 }
             }
-            for (int i = tid; i < 16 * (DK / 4); i += THREADS) {
-                const int e = i / (DK / 4), c = 4 * (i % (DK / 4));
-                f32x4 kv = zero4();
-                if (e < ne) {
-                    kv = load4(a.tape.k + ((e0 + eb + e) * Hqk + hq) * DK + c);
-                    if constexpr (KDA)
-                        kv *= load4(kt + e * LDK + c);
-                }
-                *(f32x4 *)(kt + e * LDK + c) = kv;
-            }
-            __syncthreads();
-            {  // scores of the rows with the 16 keys; a wave takes a row tile and channels
-                const int mt = wave % MT, part = wave / MT;
-                f32x4 sc = zero4();
 #pragma unroll
-                for (int cc = 0; cc < DK / (16 * S::KS); ++cc) {
-                    const int c = part * (DK / S::KS) + 16 * cc + 4 * g4;
-                    const f32x4 av = load4(kq + (16 * mt + c16) * LDK + c);
-                    const f32x4 bv = load4(kt + c16 * LDK + c);
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        sc = mfma4(av[i], bv[i], sc);
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    sp[(part * R + 16 * mt + 4 * g4 + r) * S::LDS_ + c16] = sc[r];
-            }
-            __syncthreads();
-            f32x4 av[MT];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const int m = 16 * mt + c16, tok = m % TOK;
-                const bool mine = tok / Tn == s && tok < nt;
-                f32x4 v = zero4();
-#pragma unroll
-                for (int p = 0; p < S::KS; ++p)
-                    v += load4(sp + (p * R + m) * S::LDS_ + 4 * g4);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int e = 4 * g4 + i;
+                for (int r = 0; r < 4; ++r) {
+                    const int m = 16 * mt + 4 * g4 + r, tok = m % TOK;
                     float f = 1.f;
                     if constexpr (!KDA)
-                        f = __expf(gam[mine ? tok : 0] + suf[e < ne ? e : 0]);
-                    av[mt][i] = mine && e < ne ? v[i] * f : 0.f;
+                        f = __expf(gam[tok < nt ? tok : 0] + gs);
+                    sp[(wave * R + m) * S::LDS_ + c16] = sc[mt][r] * f;
                 }
-            }
-            // the waves of one column group take every RS-th entry
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i % S::RS != rs % 4)
-                    continue;
-                const int e = 4 * g4 + i;
-                f32x4 dv = zero4();
-                if (e < ne)
-                    dv = load4(a.tape.d + ((e0 + eb + e) * H + head) * DV + 64 * cg + 4 * c16);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        add[mt][j] = mfma4(av[mt][i], dv[j], add[mt][j]);
-            }
-            __syncthreads();
         }
-        if constexpr (KDA) {
-            if (tid < DK)
-                et[s * DK + tid] = __expf(run);
-        } else if (tid == 0)
-            tot[s] = run;
-        // only the stream's own rows: what its entries hold reaches no other stream
+        __syncthreads();
+        // the log-decay over the blocks so far, for the next round and the state
+        if (tid < (KDA ? DK : 1)) {
+            for (int w = 0; w < WAVES && blk0 + w < nblk; ++w) {
+                int sw = 0, hw = 1;
+                block_at(blk0 + w, sw, hw);
+                run[sw * (KDA ? DK : 1) + tid] += bt[w * (KDA ? DK : 1) + tid];
+            }
+        }
+        for (int w = grp; w < WAVES && blk0 + w < nblk; w += G) {
+            int sw = 0, hw = 1;
+            block_at(blk0 + w, sw, hw);
+            const int lo = sw * Tn, up = lo + Tn;
+            const float *dp = a.tape.d + (((int64_t)(b0 + sw) * cap + hw - 1) * H + head) * DV + col;
+            float dx[16];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+            for (int i = 0; i < 16; ++i)
+                dx[i] = i < hw ? dp[-(int64_t)i * H * DV] : 0.f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int tok = (16 * mt + 4 * g4 + r) % TOK;
-                if (tok / Tn == s) {
+            for (int m = 0; m < TOK; ++m) {
+                if (m < lo || m >= up)
+                    continue;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[mt][j][r] = add[mt][j][r];
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 xk = load4(sp + (w * R + m) * S::LDS_ + 4 * i);
+                    const f32x4 xq = load4(sp + (w * R + TOK + m) * S::LDS_ + 4 * i);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (4 * i + j < hw) {
+                            hist[m] += xk[j] * dx[4 * i + j];
+                            hist[TOK + m] += xq[j] * dx[4 * i + j];
+                        }
+                    }
                 }
             }
+        }
+        __syncthreads();
     }
-    __syncthreads();
 
-    // ---- the state ----------------------------------------------------------------------
+    // ---- the state, 64 columns and RW rows per wave: lane (g4, c16) loads 4 adjacent columns
+    // of the rows 4 g4 + i, which serve 4 products of 16 columns each ------------------------
+    f32x4 acc[MT][4];
     {
+        f32x4 hr[S::RW / 4];
+        const float *hp = a.h_ptrs[pfx] + (int64_t)head * DK * DV +
+                          (int64_t)(rs * S::RW + 4 * g4) * DV + 64 * cg + 4 * c16;
+#pragma unroll
+        for (int i = 0; i < S::RW / 4; ++i)
+            hr[i] = load_nt4(hp + (int64_t)(16 * (i / 4) + i % 4) * DV);
+        __syncthreads();
         float f[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const int tok = (16 * mt + c16) % TOK;
             f[mt] = 1.f;
             if constexpr (!KDA)
-                f[mt] = tok < nt ? __expf(gam[tok] + tot[tok / Tn]) : 0.f;
+                f[mt] = tok < nt ? __expf(gam[tok] + run[tok / Tn]) : 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[mt][j] = zero4();
         }
 #pragma unroll
         for (int ss = 0; ss < S::RW / 16; ++ss) {
@@ -479,9 +550,10 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
             for (int mt = 0; mt < MT; ++mt) {
                 const int tok = (16 * mt + c16) % TOK;
                 av[mt] = load4(kq + (16 * mt + c16) * LDK + c);
-                if constexpr (KDA)
-                    av[mt] *= tok < nt ? load4(et + (tok / Tn) * DK + c) : zero4();
-                else
+                if constexpr (KDA) {
+                    const f32x4 x = load4(run + (tok < nt ? tok / Tn : 0) * DK + c);
+                    av[mt] *= f32x4{__expf(x.x), __expf(x.y), __expf(x.z), __expf(x.w)};
+                } else
                     av[mt] *= f[mt];
             }
 #pragma unroll
@@ -501,52 +573,71 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
             *(f32x4 *)(y + (rs * R + 16 * mt + 4 * g4 + r) * DV + 64 * cg + 4 * c16) =
                 f32x4{acc[mt][0][r], acc[mt][1][r], acc[mt][2][r], acc[mt][3][r]};
     __syncthreads();
+    if (nblk > 0) {
+#pragma unroll
+        for (int m = 0; m < R; ++m)
+            if (m % TOK < nt)
+                y[(grp * R + m) * DV + col] += hist[m];
+        __syncthreads();
+    }
 
     // ---- the new tokens in order, a thread per column ------------------------------------
-    {
-        constexpr int G = THREADS / DV;
-        const int c = tid % DV;
-        for (int s = tid / DV; s < ns; s += G) {
-            if (slen[s] < 0)
-                continue;
-            for (int t = 0; t < Tn; ++t) {
-                const int tok = s * Tn + t;
-                float yk = 0.f, yq = 0.f;
+    for (int s = grp; s < ns; s += G) {
+        if (slen[s] < 0)
+            continue;
+        const int lo = s * Tn;
+        float yk[TOK], yq[TOK];
 #pragma unroll
-                for (int p = 0; p < S::RS; ++p) {
-                    yk += y[(p * R + tok) * DV + c];
-                    yq += y[(p * R + TOK + tok) * DV + c];
-                }
-                for (int j = 0; j < t; ++j) {
-                    const float dj = vd[(s * Tn + j) * DV + c];
-                    yk += co[tok * TOK + s * Tn + j] * dj;
-                    yq += co[(TOK + tok) * TOK + s * Tn + j] * dj;
-                }
-                const float d = bet[tok] * (vd[tok * DV + c] - yk);
-                vd[tok * DV + c] = d;
-                a.tape.d[(((int64_t)(b0 + s) * cap + slen[s] + t) * H + head) * DV + c] = d;
-                y[(TOK + tok) * DV + c] = yq + co[(TOK + tok) * TOK + tok] * d;
+        for (int t = 0; t < TOK; ++t) {
+            if (t >= Tn)
+                break;
+            yk[t] = 0.f, yq[t] = 0.f;
+#pragma unroll
+            for (int p = 0; p < S::RS; ++p) {
+                yk[t] += y[(p * R + lo + t) * DV + col];
+                yq[t] += y[(p * R + TOK + lo + t) * DV + col];
             }
         }
+        float *dp = a.tape.d + (((int64_t)(b0 + s) * cap + slen[s]) * H + head) * DV + col;
+        float *op = a.o + ((row0 + lo) * H + head) * DV + col;
+#pragma unroll
+        for (int t = 0; t < TOK; ++t) {
+            if (t >= Tn)
+                break;
+            const float d = bet[lo + t] * (vd[(lo + t) * DV + col] - yk[t]);
+            dp[(int64_t)t * H * DV] = d;
+#pragma unroll
+            for (int u = t; u < TOK; ++u) {
+                if (u >= Tn)
+                    break;
+                if (u > t)
+                    yk[u] += co[(lo + u) * TOK + lo + t] * d;
+                yq[u] += co[(TOK + lo + u) * TOK + lo + t] * d;
+            }
+            if (a.z)
+                y[(TOK + lo + t) * DV + col] = yq[t];
+            else
+                op[(int64_t)t * H * DV] = yq[t];
+        }
     }
+    if (!a.z)
+        return;
     __syncthreads();
 
-    // ---- o, through the output gate if asked ---------------------------------------------
+    // ---- o through the output gate -------------------------------------------------------
     constexpr int L = DV / 4;
     for (int tok = tid / L; tok < nt; tok += THREADS / L) {
         const int l = tid % L;
         if (slen[tok / Tn] < 0)
             continue;
         f32x4 o = load4(y + (TOK + tok) * DV + 4 * l);
-        if (a.z) {
-            const f32x4 z = load4((const T *)a.z + (row0 + tok) * a.ld_z + (int64_t)head * DV + 4 * l);
-            const f32x4 w = load4(a.norm_w + 4 * l);
-            const float ss = group_sum<L>(o.x * o.x + o.y * o.y + o.z * o.z + o.w * o.w);
-            const float inv = 1.f / sqrtf(ss * (1.f / DV) + a.norm_eps);
+        const f32x4 z = load4((const T *)a.z + (row0 + tok) * a.ld_z + (int64_t)head * DV + 4 * l);
+        const f32x4 w = load4(a.norm_w + 4 * l);
+        const float ss = group_sum<L>(o.x * o.x + o.y * o.y + o.z * o.z + o.w * o.w);
+        const float inv = __builtin_amdgcn_rsqf(ss * (1.f / DV) + a.norm_eps);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                o[i] *= inv * w[i] * silu(z[i]);
-        }
+        for (int i = 0; i < 4; ++i)
+            o[i] *= inv * w[i] * silu(z[i]);
         *(f32x4 *)(a.o + ((row0 + tok) * H + head) * DV + 4 * l) = o;
     }
 }
