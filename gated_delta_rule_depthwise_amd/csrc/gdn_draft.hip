@@ -119,44 +119,46 @@ template <int N> __device__ __forceinline__ float group_sum(float x)
 template <int DK, int DV, bool KDA, int TOK> struct DraftShape {
     static constexpr int R = 2 * TOK;          // rows of the products
     static constexpr int MT = R / 16;          // 16-row MFMA tiles
-    static constexpr int NS = TOK < 8 ? TOK : 8;  // streams per tile, at most
+    static constexpr int NS = 8;               // streams per tile, at most
     static constexpr int CG = DV / 64;         // 64-column groups, one wave (or more) each
     static constexpr int RS = WAVES / CG;      // waves that share a column group's rows
     static constexpr int RW = DK / RS;         // rows of h per wave
     static constexpr int LDK = DK + 4;         // row stride of the key tile
     static constexpr int LDS_ = 20;            // row stride of the score tiles
     static constexpr int G = THREADS / DV;     // threads per column
+    static constexpr int EG = 16 / G;          // entries of a tape block per thread of a column
+    static constexpr int GW = KDA ? DK : 1;    // log-gates per token
     static_assert(G == RS, "a part of Y per thread of a column");
-    // LDS, in floats; the partial products Y overlay everything that is dead by then
+    // LDS, in floats; the partial products Y overlay what is dead by then
     static constexpr int KQ = 0;
-    static constexpr int SP = KQ + R * LDK;                   // scores of a block per wave
+    static constexpr int Y = KQ + R * LDK;
+    static constexpr int SP = Y;                              // scores of a block per wave
     static constexpr int BT = SP + WAVES * R * LDS_;          // log-decay over a wave's block
-    static constexpr int GK = BT + WAVES * (KDA ? DK : 1);    // KDA: new tokens' log-gates
+    static constexpr int GK = BT + WAVES * GW;                // KDA: new tokens' log-gates
     static constexpr int END1 = GK + (KDA ? TOK * DK : 0);
-    static constexpr int Y = 0;
-    static constexpr int END2 = RS * R * DV;
+    static constexpr int END2 = Y + RS * R * DV;
     static constexpr int RUN = END1 > END2 ? END1 : END2;     // log-decay over a tape's newer blocks
-    static constexpr int VD = RUN + NS * (KDA ? DK : 1);      // v
+    static constexpr int VD = RUN + NS * GW;                  // v
     static constexpr int CO = VD + TOK * DV;                  // coefficients among new tokens
     static constexpr int SM = CO + R * TOK;                   // small: see the kernel
-    static constexpr int TOTAL = SM + 2 * TOK + NS;
-    static_assert(TOTAL * 4 <= 65536, "static LDS");
+    static constexpr int TOTAL = SM + 3 * TOK + NS;
     static_assert(RW % 16 == 0 && DK % 16 == 0, "tile map");
 };
 
 template <typename T, int DK, int DV, bool KDA, int K, int TOK>
-__global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int ntile)
+__global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 : 2) draft_kernel(const DraftArgs a, int ntile)
 {
     using S = DraftShape<DK, DV, KDA, TOK>;
     using P = Pair<T>;
     constexpr int W = K > 0 ? K - 1 : 0;
-    constexpr int R = S::R, MT = S::MT, NS = S::NS, LDK = S::LDK, G = S::G;
+    constexpr int R = S::R, MT = S::MT, NS = S::NS, LDK = S::LDK, EG = S::EG, GW = S::GW;
     __shared__ __align__(16) float sm[S::TOTAL];
     float *const kq = sm + S::KQ, *const sp = sm + S::SP, *const bt = sm + S::BT;
     float *const gk = sm + S::GK, *const y = sm + S::Y, *const run = sm + S::RUN;
     float *const vd = sm + S::VD, *const co = sm + S::CO;
     float *const gam = sm + S::SM;        // [TOK] log-gates through each new token (GDN)
-    float *const bet = gam + TOK;         // [TOK]
+    float *const gnew = gam + TOK;        // [TOK] log-gates of the new tokens (GDN)
+    float *const bet = gnew + TOK;        // [TOK]
     int *const slen = (int *)(bet + TOK); // [NS] tape lengths, -1: stream left out
 
     const int H = a.H, Hqk = a.Hqk, Tn = a.T, cap = a.tape.cap;
@@ -174,40 +176,57 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c16 = lane & 15, g4 = lane >> 4;
     const int cg = wave % S::CG, rs = wave / S::CG;
+    const int col = tid % DV, grp = tid / DV;
+    // stream of a token of the tile: exact for tok < 16, T <= 16 (the rounding of 256/T up
+    // adds less than 16/256, which is below 1/T)
+    const int inv_t = (256 + Tn - 1) / Tn;
+    const auto stream_of = [&](int tok) { return tok * inv_t >> 8; };
 
-    // a stream's tape length, -1 where the stream is left out
-    const auto tape_len = [&](int s) {
-        const int n = a.tape.len[b0 + s];
-        return n < 0 || n > cap - Tn ? -1 : n;
-    };
-    if (tid < ns) {
-        const int n = tape_len(tid);
-        if (n < 0 && a.dbg && head == 0)
-            atomicOr(a.dbg, GDN_BAD_TAPE);
-        slen[tid] = n;
+    // tape lengths, -1 where a stream is left out: lane s of every wave has that of stream s
+    int len_s = -1, nblk = 0;
+    if (lane < ns) {
+        len_s = a.tape.len[b0 + lane];
+        len_s = len_s < 0 || len_s > cap - Tn ? -1 : len_s;
     }
+    if (tid < NS) {
+        slen[tid] = len_s;
+        if (tid < ns && len_s < 0 && a.dbg && head == 0)
+            atomicOr(a.dbg, GDN_BAD_TAPE);
+    }
+    const auto tape_len = [&](int s) { return __builtin_amdgcn_readlane(len_s, s); };
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+        nblk += (tape_len(s) + 15) >> 4;
+    // The tapes are walked in blocks of 16 entries of one stream, newest first; block blk of
+    // the tile's streams: its stream, and one past its newest entry.
+    const auto block_at = [&](int blk, int &s, int &hi) {
+        s = 0, hi = 1;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int n = tape_len(i), nb = (n + 15) >> 4;
+            if (blk >= 0 && blk < nb)
+                s = i, hi = n - 16 * blk;
+            blk -= nb;
+        }
+    };
 
-    // ---- front end: a thread takes two adjacent channels of every token; all its loads go
-    // out together -------------------------------------------------------------------------
+    // ---- loads of the front end: a thread takes two adjacent channels of every token --------
     constexpr int CP = (2 * DK + DV) / 2;
     static_assert(CP <= THREADS, "front end map");
+    const int fc = 2 * tid, sec = fc < DK ? 0 : fc < 2 * DK ? 1 : 2;
+    const int fe = sec == 0 ? fc : sec == 1 ? fc - DK : fc - 2 * DK;
+    const int64_t fcol = sec == 2 ? (int64_t)head * DV + fe : (int64_t)hq * DK + fe;
+    const int64_t ch = (sec == 0 ? 0 : (int64_t)sec * Hqk * DK) + fcol;
+    typename P::raw raw[TOK], old[TOK][W > 0 ? W : 1];
+    float2 w[K > 0 ? K : 1];
     if (tid < CP) {
-        const int c = 2 * tid;
-        const int sec = c < DK ? 0 : c < 2 * DK ? 1 : 2;
-        const int e = sec == 0 ? c : sec == 1 ? c - DK : c - 2 * DK;
-        const T *src = (const T *)(sec == 0 ? a.q : sec == 1 ? a.k : a.v);
-        const int64_t col = sec == 2 ? (int64_t)head * DV + e : (int64_t)hq * DK + e;
-        const int64_t ch = (sec == 0 ? 0 : (int64_t)sec * Hqk * DK) + col;
-        float *dst = sec == 2 ? vd + e : kq + (sec == 0 ? TOK * LDK : 0) + e;
-        const int ldd = sec == 2 ? DV : LDK;
-        typename P::raw raw[TOK], old[TOK][W > 0 ? W : 1];
+        const T *src = (const T *)(sec == 0 ? a.q : sec == 1 ? a.k : a.v) + row0 * a.ld + fcol;
 #pragma unroll
         for (int tok = 0; tok < TOK; ++tok) {
             raw[tok] = typename P::raw{};
             if (tok < nt)
-                raw[tok] = *(const typename P::raw *)(src + (row0 + tok) * a.ld + col);
+                raw[tok] = *(const typename P::raw *)(src + tok * a.ld);
         }
-        float2 w[K > 0 ? K : 1], win[W > 0 ? W : 1];
         if constexpr (K > 0) {
 #pragma unroll
             for (int i = 0; i < K; ++i)
@@ -238,58 +257,99 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
                 }
             }
         }
-        int s = 0, t = 0;
-#pragma unroll
-        for (int tok = 0; tok < TOK; ++tok) {
-            float x0 = P::lo(raw[tok]), x1 = P::hi(raw[tok]);
-            if (tok < nt) {
-                if constexpr (K > 0) {
-                    if (t == 0) {
-#pragma unroll
-                        for (int i = 0; i < W; ++i)
-                            win[i] = float2{P::lo(old[tok][i]), P::hi(old[tok][i])};
-                    }
-                    float a0 = w[K - 1].x * x0, a1 = w[K - 1].y * x1;
-#pragma unroll
-                    for (int i = 0; i < W; ++i)
-                        a0 += w[i].x * win[i].x, a1 += w[i].y * win[i].y;
-#pragma unroll
-                    for (int i = 0; i + 1 < W; ++i)
-                        win[i] = win[i + 1];
-                    win[W - 1] = float2{x0, x1};
-                    x0 = silu(a0), x1 = silu(a1);
-                    const int n = tape_len(s);
-                    if (n >= 0 && (sec == 2 || own_qk))
-                        *(typename P::raw *)((T *)a.tape.raw +
-                                             ((int64_t)(b0 + s) * cap + n + t) * cd + ch) = raw[tok];
-                }
-                if (++t == Tn)
-                    t = 0, ++s;
-            }
-            dst[tok * ldd] = x0, dst[tok * ldd + 1] = x1;
-        }
     }
-    // ---- log-gates and betas of the new tokens ---------------------------------------------
+    if (tid >= THREADS - TOK && tid < THREADS - TOK + nt) {
+        const int tok = tid - (THREADS - TOK);
+        bet[tok] = a.beta[(row0 + tok) * H + head];
+        if constexpr (!KDA)
+            gnew[tok] = a.g[(row0 + tok) * H + head];
+    }
     if constexpr (KDA) {
         for (int i = tid; i < nt * (DK / 4); i += THREADS) {
             const int tok = i / (DK / 4), c = 4 * (i % (DK / 4));
             *(f32x4 *)(gk + tok * DK + c) = load4(a.g + ((row0 + tok) * H + head) * DK + c);
         }
     }
-    if (tid >= THREADS - TOK && tid < THREADS - TOK + nt) {
-        const int tok = tid - (THREADS - TOK);
-        bet[tok] = a.beta[(row0 + tok) * H + head];
-        if constexpr (!KDA)
-            gam[tok] = a.g[(row0 + tok) * H + head];
-    }
-    for (int i = tid; i < NS * (KDA ? DK : 1); i += THREADS)
+    for (int i = tid; i < NS * GW; i += THREADS)
         run[i] = 0.f;
+
+    // ---- loads of the first tape blocks: a wave's keys and log-gates, a thread's updates ----
+    f32x4 kf[DK / 16], ge[KDA ? DK / 16 : 1];
+    float gs = 0.f, dx[2][EG];
+    int ws = 0, whi = 1;  // the wave's block: stream, one past its newest entry
+    const auto load_keys = [&](int blk) {
+        block_at(blk, ws, whi);
+        const int e = whi - 1 - c16;  // lane c16: the c16-th newest entry of the block
+        const int64_t at = (int64_t)(b0 + ws) * cap + (e > 0 ? e : 0);
+        const float *kp = a.tape.k + (at * Hqk + hq) * DK + 4 * g4;
+#pragma unroll
+        for (int i = 0; i < DK / 16; ++i)
+            kf[i] = load4(kp + 16 * i);
+        if constexpr (KDA) {
+            const float *gp = a.tape.g + (at * H + head) * DK + 4 * g4;
+#pragma unroll
+            for (int i = 0; i < DK / 16; ++i)
+                ge[i] = load4(gp + 16 * i);
+        } else
+            gs = a.tape.g[at * H + head];
+    };
+    const auto load_updates = [&](int blk, float *d) {
+        int s, hi;
+        block_at(blk, s, hi);
+        const float *dp = a.tape.d + (((int64_t)(b0 + s) * cap + hi - 1) * H + head) * DV + col;
+#pragma unroll
+        for (int i = 0; i < EG; ++i) {
+            const int e = grp * EG + i;
+            d[i] = e < hi ? dp[-(int64_t)e * H * DV] : 0.f;
+        }
+    };
+    constexpr bool EARLY = !KDA || DK == 64;  // registers for the first keys from here on
+    if (EARLY && wave < nblk)
+        load_keys(wave);
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+        if (p < nblk)
+            load_updates(p, dx[p]);
+
+    // ---- front end ---------------------------------------------------------------------------
+    if (tid < CP) {
+        float *dst = sec == 2 ? vd + fe : kq + (sec == 0 ? TOK * LDK : 0) + fe;
+        const int ldd = sec == 2 ? DV : LDK;
+        float2 win[W > 0 ? W : 1];
+        int s = 0, t = 0, n = 0;
+#pragma unroll
+        for (int tok = 0; tok < TOK; ++tok) {
+            float x0 = P::lo(raw[tok]), x1 = P::hi(raw[tok]);
+            if (K > 0 && tok < nt) {
+                if (t == 0) {
+                    n = tape_len(s);
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        win[i] = float2{P::lo(old[tok][i]), P::hi(old[tok][i])};
+                }
+                float a0 = w[K > 0 ? K - 1 : 0].x * x0, a1 = w[K > 0 ? K - 1 : 0].y * x1;
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    a0 += w[i].x * win[i].x, a1 += w[i].y * win[i].y;
+#pragma unroll
+                for (int i = 0; i + 1 < W; ++i)
+                    win[i] = win[i + 1];
+                win[W > 0 ? W - 1 : 0] = float2{x0, x1};
+                x0 = silu(a0), x1 = silu(a1);
+                if (n >= 0 && (sec == 2 || own_qk))
+                    *(typename P::raw *)((T *)a.tape.raw + ((int64_t)(b0 + s) * cap + n + t) * cd + ch) = raw[tok];
+                if (++t == Tn)
+                    t = 0, ++s;
+            }
+            *(float2 *)(dst + tok * ldd) = float2{x0, x1};
+        }
+    }
     __syncthreads();
 
-    // ---- L2 and scale: 16 lanes per row; the new entries' keys and log-gates ----------------
+    // ---- L2 and scale: 16 lanes per row; the new entries' keys ------------------------------
 #pragma unroll
-    for (int m = tid >> 4; m < R; m += THREADS / 16) {
-        const int tok = m % TOK, l = tid & 15;
+    for (int m0 = 0; m0 < R; m0 += THREADS / 16) {
+        const int m = m0 + (tid >> 4), tok = m % TOK, l = tid & 15;
         float *x = kq + m * LDK + 4 * l;
         f32x4 v[DK / 64];
         float ss = 0.f;
@@ -302,66 +362,79 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
         float mul = a.do_l2 ? __builtin_amdgcn_rsqf(ss + a.eps) : 1.f;
         if (m >= TOK)
             mul *= a.scale;
-        const int s = tok / Tn;
-        const bool put = m < TOK && own_qk && tok < nt && slen[s < NS ? s : 0] >= 0;
+        const int s = stream_of(tok), n = tok < nt ? slen[s] : -1;
 #pragma unroll
         for (int i = 0; i < DK / 64; ++i) {
-            v[i] *= mul;
-            if (tok >= nt)
-                v[i] = zero4();
+            v[i] = tok < nt ? v[i] * mul : zero4();
             *(f32x4 *)(x + 64 * i) = v[i];
-            if (put)
-                *(f32x4 *)(a.tape.k + (((int64_t)(b0 + s) * cap + slen[s] + tok - s * Tn) * Hqk + hq) * DK +
+            if (m < TOK && own_qk && n >= 0)
+                *(f32x4 *)(a.tape.k + (((int64_t)(b0 + s) * cap + n + tok - s * Tn) * Hqk + hq) * DK +
                            4 * l + 64 * i) = v[i];
         }
     }
-    // running sums of the log-gates within each stream's new tokens
+    // running sums of the log-gates within each stream's new tokens; their tape entries
     if constexpr (KDA) {
         if (tid < DK) {
-            int s = 0, t = 0;
+            float gv[TOK];
+#pragma unroll
+            for (int tok = 0; tok < TOK; ++tok)
+                gv[tok] = tok < nt ? gk[tok * DK + tid] : 0.f;
+            int s = 0, t = 0, n = 0;
             float sum = 0.f;
-            for (int tok = 0; tok < nt; ++tok) {
-                const float gv = gk[tok * DK + tid];
-                if (slen[s] >= 0)
-                    a.tape.g[(((int64_t)(b0 + s) * cap + slen[s] + t) * H + head) * DK + tid] = gv;
-                sum = (t == 0 ? 0.f : sum) + gv;
-                gk[tok * DK + tid] = sum;
-                if (++t == Tn)
-                    t = 0, ++s;
+#pragma unroll
+            for (int tok = 0; tok < TOK; ++tok) {
+                if (tok < nt) {
+                    if (t == 0)
+                        n = tape_len(s), sum = 0.f;
+                    if (n >= 0)
+                        a.tape.g[(((int64_t)(b0 + s) * cap + n + t) * H + head) * DK + tid] = gv[tok];
+                    sum += gv[tok];
+                    gk[tok * DK + tid] = sum;
+                    if (++t == Tn)
+                        t = 0, ++s;
+                }
             }
         }
-    } else if (tid < ns) {
+    } else if (tid < nt) {
+        const int s = stream_of(tid), n = slen[s];
         float sum = 0.f;
-        for (int t = 0; t < Tn; ++t) {
-            const float gv = gam[tid * Tn + t];
-            if (slen[tid] >= 0)
-                a.tape.g[((int64_t)(b0 + tid) * cap + slen[tid] + t) * H + head] = gv;
-            gam[tid * Tn + t] = sum += gv;
+#pragma unroll
+        for (int j = 0; j < TOK; ++j) {
+            const float gv = gnew[j];
+            if (j >= s * Tn && j <= tid)
+                sum += gv;
         }
+        gam[tid] = sum;
+        if (n >= 0)
+            a.tape.g[((int64_t)(b0 + s) * cap + n + tid - s * Tn) * H + head] = gnew[tid];
     }
     __syncthreads();
 
-    // ---- coefficients among the new tokens: 16 lanes per pair ----------------------------
-    for (int idx = tid >> 4; idx < R * TOK; idx += THREADS / 16) {
-        const int m = idx / TOK, j = idx % TOK, tok = m % TOK, l = tid & 15;
-        if (tok >= nt || tok / Tn != j / Tn || (m < TOK ? j >= tok : j > tok))
-            continue;
-        float sum = 0.f;
+    // ---- coefficients among the new tokens: 16 lanes per pair (x, y) of a stream's tokens:
+    // y < x: key y in d_x; y >= x: key x in o_y --------------------------------------------
+    {
+        const int per = Tn * Tn, inv_p = (65536 + per - 1) / per, inv_x = (65536 + Tn - 1) / Tn, l = tid & 15;
+        for (int idx = tid >> 4; idx < ns * per; idx += THREADS / 16) {
+            const int s = idx * inv_p >> 16, r = idx - s * per, xx = r * inv_x >> 16, yy = r - xx * Tn;
+            const int tok = s * Tn + (yy < xx ? xx : yy), j = s * Tn + (yy < xx ? yy : xx);
+            const int m = (yy < xx ? 0 : TOK) + tok;
+            float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < DK / 64; ++i) {
-            const f32x4 x = load4(kq + m * LDK + 4 * l + 64 * i);
-            f32x4 kj = load4(kq + j * LDK + 4 * l + 64 * i);
-            if constexpr (KDA) {
-                const f32x4 e = load4(gk + tok * DK + 4 * l + 64 * i) - load4(gk + j * DK + 4 * l + 64 * i);
-                kj.x *= __expf(e.x), kj.y *= __expf(e.y), kj.z *= __expf(e.z), kj.w *= __expf(e.w);
+            for (int i = 0; i < DK / 64; ++i) {
+                const f32x4 x = load4(kq + m * LDK + 4 * l + 64 * i);
+                f32x4 kj = load4(kq + j * LDK + 4 * l + 64 * i);
+                if constexpr (KDA) {
+                    const f32x4 e = load4(gk + tok * DK + 4 * l + 64 * i) - load4(gk + j * DK + 4 * l + 64 * i);
+                    kj *= f32x4{__expf(e.x), __expf(e.y), __expf(e.z), __expf(e.w)};
+                }
+                sum += x.x * kj.x + x.y * kj.y + x.z * kj.z + x.w * kj.w;
             }
-            sum += x.x * kj.x + x.y * kj.y + x.z * kj.z + x.w * kj.w;
+            sum = row_sum(sum);
+            if constexpr (!KDA)
+                sum *= __expf(gam[tok] - gam[j]);
+            if (l == 0)
+                co[m * TOK + j] = sum;
         }
-        sum = row_sum(sum);
-        if constexpr (!KDA)
-            sum *= __expf(gam[tok] - gam[j]);
-        if (l == 0)
-            co[idx] = sum;
     }
     if constexpr (KDA) {  // keys and queries take the decay through their token
         __syncthreads();
@@ -373,57 +446,27 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
                 *(f32x4 *)x = load4(x) * f32x4{__expf(e.x), __expf(e.y), __expf(e.z), __expf(e.w)};
             }
         }
-        __syncthreads();
     }
 
-    // ---- the tapes, in blocks of 16 entries of one stream, newest first: each round every
-    // wave scores one block against all rows; then a thread per column adds the block's
-    // updates to the rows of the block's own stream (so what a tape holds reaches no other
-    // stream, be it NaN) ---------------------------------------------------------------------
-    const int col = tid % DV, grp = tid / DV;
+    // ---- the tapes: each round every wave scores one block against all rows; then a thread
+    // per column adds the block's updates to the rows of the block's own stream (so what a
+    // tape holds reaches no other stream, be it NaN) ------------------------------------------
     float hist[R];
 #pragma unroll
     for (int m = 0; m < R; ++m)
         hist[m] = 0.f;
-    int nblk = 0;
-    for (int s = 0; s < ns; ++s)
-        nblk += slen[s] > 0 ? (slen[s] + 15) >> 4 : 0;
-    nblk = __builtin_amdgcn_readfirstlane(nblk);
-    // stream of a block, and one past its newest entry
-    const auto block_at = [&](int blk, int &s, int &hi) {
-        s = 0;
-        for (; s < ns; ++s) {
-            const int n = __builtin_amdgcn_readfirstlane(slen[s]);
-            const int nb = n > 0 ? (n + 15) >> 4 : 0;
-            if (blk < nb) {
-                hi = n - 16 * blk;
-                return;
-            }
-            blk -= nb;
-        }
-    };
     for (int blk0 = 0; blk0 < nblk; blk0 += WAVES) {
-        int s = 0, hi = 1;
         const bool act = blk0 + wave < nblk;
-        f32x4 kf[DK / 16], ge[KDA ? DK / 16 : 1];
-        float gs = 0.f;
-        if (act) {
-            block_at(blk0 + wave, s, hi);
-            const int e = hi - 1 - c16;  // lane c16: the c16-th newest entry of the block
-            const int64_t at = (int64_t)(b0 + s) * cap + (e > 0 ? e : 0);
-            const float *kp = a.tape.k + (at * Hqk + hq) * DK + 4 * g4;
-#pragma unroll
-            for (int i = 0; i < DK / 16; ++i)
-                kf[i] = load4(kp + 16 * i);
-            // log-decay over the block's newer entries, and over the whole block
+        if (!EARLY && act)
+            load_keys(blk0 + wave);
+        if (act) {  // log-decay over the block's newer entries, and over the whole block
+            const bool in = whi - 1 - c16 >= 0;
             if constexpr (KDA) {
-                const float *gp = a.tape.g + (at * H + head) * DK + 4 * g4;
 #pragma unroll
                 for (int i = 0; i < DK / 16; ++i) {
-                    ge[i] = e >= 0 ? load4(gp + 16 * i) : zero4();
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        ge[i][j] = row_scan(ge[i][j]);
+                        ge[i][j] = row_scan(in ? ge[i][j] : 0.f);
                     if (c16 == 15)
                         *(f32x4 *)(bt + wave * DK + 16 * i + 4 * g4) = ge[i];
 #pragma unroll
@@ -431,7 +474,7 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
                         ge[i][j] = dpp<DPP_SHR + 1>(ge[i][j]);
                 }
             } else {
-                gs = row_scan(e >= 0 ? a.tape.g[at * H + head] : 0.f);
+                gs = row_scan(in ? gs : 0.f);
                 if (lane == 15)
                     bt[wave] = gs;
                 gs = dpp<DPP_SHR + 1>(gs);
@@ -439,29 +482,31 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
         }
         __syncthreads();
         if (act) {
-            // the blocks of this round before this wave's that are of its stream: the last
-            // (hi's distance from the tape's end tells how many) of the waves below
-            int newer = (__builtin_amdgcn_readfirstlane(slen[s]) - hi) >> 4;
+            // the waves before this one with newer blocks of its stream
+            int newer = (tape_len(ws) - whi) >> 4;
             newer = newer < wave ? newer : wave;
             f32x4 sc[MT];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
                 sc[mt] = zero4();
             if constexpr (!KDA) {
-                gs += run[s];
-                for (int w = wave - newer; w < wave; ++w)
-                    gs += bt[w];
+                gs += run[ws];
+                for (int v = wave - newer; v < wave; ++v)
+                    gs += bt[v];
             }
 #pragma unroll
             for (int i = 0; i < DK / 16; ++i) {
                 if constexpr (KDA) {
-                    f32x4 x = ge[i] + load4(run + s * DK + 16 * i + 4 * g4);
-                    for (int w = wave - newer; w < wave; ++w)
-                        x += load4(bt + w * DK + 16 * i + 4 * g4);
+                    f32x4 x = ge[i] + load4(run + ws * DK + 16 * i + 4 * g4);
+                    for (int v = wave - newer; v < wave; ++v)
+                        x += load4(bt + v * DK + 16 * i + 4 * g4);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         kf[i][j] *= __expf(x[j]);
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < DK / 16; ++i)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     const f32x4 av = load4(kq + (16 * mt + c16) * LDK + 16 * i + 4 * g4);
@@ -469,7 +514,6 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
                     for (int j = 0; j < 4; ++j)
                         sc[mt] = mfma4(av[j], kf[i][j], sc[mt]);
                 }
-            }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -482,36 +526,44 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
                 }
         }
         __syncthreads();
+        if (EARLY && blk0 + WAVES + wave < nblk)
+            load_keys(blk0 + WAVES + wave);
         // the log-decay over the blocks so far, for the next round and the state
-        if (tid < (KDA ? DK : 1)) {
-            for (int w = 0; w < WAVES && blk0 + w < nblk; ++w) {
-                int sw = 0, hw = 1;
-                block_at(blk0 + w, sw, hw);
-                run[sw * (KDA ? DK : 1) + tid] += bt[w * (KDA ? DK : 1) + tid];
+        if (tid < GW) {
+            for (int v = 0; v < WAVES && blk0 + v < nblk; ++v) {
+                int s, hi;
+                block_at(blk0 + v, s, hi);
+                run[s * GW + tid] += bt[v * GW + tid];
             }
         }
-        for (int w = grp; w < WAVES && blk0 + w < nblk; w += G) {
-            int sw = 0, hw = 1;
-            block_at(blk0 + w, sw, hw);
-            const int lo = sw * Tn, up = lo + Tn;
-            const float *dp = a.tape.d + (((int64_t)(b0 + sw) * cap + hw - 1) * H + head) * DV + col;
-            float dx[16];
+        for (int v0 = 0; v0 < WAVES && blk0 + v0 < nblk; v0 += 2) {
+            if (blk0 + v0 > 0) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                dx[i] = i < hw ? dp[-(int64_t)i * H * DV] : 0.f;
+                for (int p = 0; p < 2; ++p)
+                    if (blk0 + v0 + p < nblk)
+                        load_updates(blk0 + v0 + p, dx[p]);
+            }
 #pragma unroll
-            for (int m = 0; m < TOK; ++m) {
-                if (m < lo || m >= up)
+            for (int p = 0; p < 2; ++p) {
+                if (blk0 + v0 + p >= nblk)
                     continue;
+                int s, hi;
+                block_at(blk0 + v0 + p, s, hi);
+                const int lo = s * Tn, up = lo + Tn;
+                const float *xp = sp + (v0 + p) * R * S::LDS_ + grp * EG;
+                // scores of entries before the tape's first are of no meaning
+                const int ne = hi - grp * EG;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x4 xk = load4(sp + (w * R + m) * S::LDS_ + 4 * i);
-                    const f32x4 xq = load4(sp + (w * R + TOK + m) * S::LDS_ + 4 * i);
+                for (int m = 0; m < TOK; ++m) {
+                    if (m < lo || m >= up)
+                        continue;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (4 * i + j < hw) {
-                            hist[m] += xk[j] * dx[4 * i + j];
-                            hist[TOK + m] += xq[j] * dx[4 * i + j];
+                    for (int i = 0; i < EG; i += 4) {
+                        const f32x4 xk = load4(xp + m * S::LDS_ + i), xq = load4(xp + (TOK + m) * S::LDS_ + i);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            hist[m] += i + j < ne ? xk[j] * dx[p][i + j] : 0.f;
+                            hist[TOK + m] += i + j < ne ? xq[j] * dx[p][i + j] : 0.f;
                         }
                     }
                 }
@@ -522,14 +574,20 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
 
     // ---- the state, 64 columns and RW rows per wave: lane (g4, c16) loads 4 adjacent columns
     // of the rows 4 g4 + i, which serve 4 products of 16 columns each ------------------------
-    f32x4 acc[MT][4];
     {
-        f32x4 hr[S::RW / 4];
+        f32x4 hr[S::RW / 4], acc[MT][4];
         const float *hp = a.h_ptrs[pfx] + (int64_t)head * DK * DV +
                           (int64_t)(rs * S::RW + 4 * g4) * DV + 64 * cg + 4 * c16;
 #pragma unroll
         for (int i = 0; i < S::RW / 4; ++i)
             hr[i] = load_nt4(hp + (int64_t)(16 * (i / 4) + i % 4) * DV);
+        // the products start from what the tapes gave: part grp of a column's threads
+        float *const yp = y + (rs * R + 4 * g4) * DV + 64 * cg + 4 * c16;
+        if (nblk > 0) {
+#pragma unroll
+            for (int m = 0; m < R; ++m)
+                y[(grp * R + m) * DV + col] = hist[m];
+        }
         __syncthreads();
         float f[MT];
 #pragma unroll
@@ -537,10 +595,14 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
             const int tok = (16 * mt + c16) % TOK;
             f[mt] = 1.f;
             if constexpr (!KDA)
-                f[mt] = tok < nt ? __expf(gam[tok] + run[tok / Tn]) : 0.f;
+                f[mt] = tok < nt ? __expf(gam[tok] + run[stream_of(tok)]) : 0.f;
+            f32x4 v[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                v[r] = nblk > 0 ? load4(yp + (16 * mt + r) * DV) : zero4();
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                acc[mt][j] = zero4();
+                acc[mt][j] = f32x4{v[0][j], v[1][j], v[2][j], v[3][j]};
         }
 #pragma unroll
         for (int ss = 0; ss < S::RW / 16; ++ss) {
@@ -551,7 +613,7 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
                 const int tok = (16 * mt + c16) % TOK;
                 av[mt] = load4(kq + (16 * mt + c16) * LDK + c);
                 if constexpr (KDA) {
-                    const f32x4 x = load4(run + (tok < nt ? tok / Tn : 0) * DK + c);
+                    const f32x4 x = load4(run + (tok < nt ? stream_of(tok) : 0) * DK + c);
                     av[mt] *= f32x4{__expf(x.x), __expf(x.y), __expf(x.z), __expf(x.w)};
                 } else
                     av[mt] *= f[mt];
@@ -564,25 +626,17 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
                     for (int j = 0; j < 4; ++j)
                         acc[mt][j] = mfma4(av[mt][i], hr[4 * ss + i][j], acc[mt][j]);
         }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *(f32x4 *)(yp + (16 * mt + r) * DV) =
+                    f32x4{acc[mt][0][r], acc[mt][1][r], acc[mt][2][r], acc[mt][3][r]};
     }
-    __syncthreads();  // Y overlays the key tiles
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            *(f32x4 *)(y + (rs * R + 16 * mt + 4 * g4 + r) * DV + 64 * cg + 4 * c16) =
-                f32x4{acc[mt][0][r], acc[mt][1][r], acc[mt][2][r], acc[mt][3][r]};
     __syncthreads();
-    if (nblk > 0) {
-#pragma unroll
-        for (int m = 0; m < R; ++m)
-            if (m % TOK < nt)
-                y[(grp * R + m) * DV + col] += hist[m];
-        __syncthreads();
-    }
 
     // ---- the new tokens in order, a thread per column ------------------------------------
-    for (int s = grp; s < ns; s += G) {
+    for (int s = grp; s < ns; s += S::G) {
         if (slen[s] < 0)
             continue;
         const int lo = s * Tn;
@@ -628,7 +682,7 @@ __global__ void __launch_bounds__(THREADS) draft_kernel(const DraftArgs a, int n
     constexpr int L = DV / 4;
     for (int tok = tid / L; tok < nt; tok += THREADS / L) {
         const int l = tid % L;
-        if (slen[tok / Tn] < 0)
+        if (slen[stream_of(tok)] < 0)
             continue;
         f32x4 o = load4(y + (TOK + tok) * DV + 4 * l);
         const f32x4 z = load4((const T *)a.z + (row0 + tok) * a.ld_z + (int64_t)head * DV + 4 * l);
