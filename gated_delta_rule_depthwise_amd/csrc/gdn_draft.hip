@@ -141,7 +141,7 @@ template <int DK, int DV, bool KDA, int TOK> struct DraftShape {
     static constexpr int VD = RUN + NS * GW;                  // v
     static constexpr int CO = VD + TOK * DV;                  // coefficients among new tokens
     static constexpr int SM = CO + R * TOK;                   // small: see the kernel
-    static constexpr int TOTAL = SM + 3 * TOK + NS;
+    static constexpr int TOTAL = SM + 3 * TOK + NS + WAVES;
     static_assert(RW % 16 == 0 && DK % 16 == 0, "tile map");
 };
 
@@ -160,9 +160,14 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
     float *const gnew = gam + TOK;        // [TOK] log-gates of the new tokens (GDN)
     float *const bet = gnew + TOK;        // [TOK]
     int *const slen = (int *)(bet + TOK); // [NS] tape lengths, -1: stream left out
+    int *const sblk = slen + NS;          // [WAVES] the streams of a round's blocks
 
     const int H = a.H, Hqk = a.Hqk, Tn = a.T, cap = a.tape.cap;
-    const int tile = blockIdx.x % ntile, ph = blockIdx.x / ntile;
+    // the tiles of one state run on one XCD (workgroups go to the 8 XCDs in turn), whose L2
+    // then serves all but the first of them
+    const int tile = (blockIdx.x >> 3) % ntile, ph = (blockIdx.x >> 3) / ntile * 8 + (blockIdx.x & 7);
+    if (ph >= (a.B / a.share) * H)
+        return;
     const int head = ph % H, pfx = ph / H;
     const int rep = H / Hqk, hq = head / rep;
     const bool own_qk = head % rep == 0;  // this workgroup writes the q/k head's tape entries
@@ -182,8 +187,9 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
     const int inv_t = (256 + Tn - 1) / Tn;
     const auto stream_of = [&](int tok) { return tok * inv_t >> 8; };
 
-    // tape lengths, -1 where a stream is left out: lane s of every wave has that of stream s
-    int len_s = -1, nblk = 0;
+    // tape lengths, -1 where a stream is left out: lane s of every wave has that of stream s,
+    // its number of blocks (16 entries, newest first) and those of the streams before it
+    int len_s = -1;
     if (lane < ns) {
         len_s = a.tape.len[b0 + lane];
         len_s = len_s < 0 || len_s > cap - Tn ? -1 : len_s;
@@ -194,20 +200,16 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
             atomicOr(a.dbg, GDN_BAD_TAPE);
     }
     const auto tape_len = [&](int s) { return __builtin_amdgcn_readlane(len_s, s); };
-#pragma unroll
-    for (int s = 0; s < NS; ++s)
-        nblk += (tape_len(s) + 15) >> 4;
-    // The tapes are walked in blocks of 16 entries of one stream, newest first; block blk of
-    // the tile's streams: its stream, and one past its newest entry.
+    const int nb_s = (len_s + 15) >> 4;
+    int upto = nb_s;
+    upto += __builtin_amdgcn_update_dpp(0, upto, DPP_SHR + 1, 0xf, 0xf, true);
+    upto += __builtin_amdgcn_update_dpp(0, upto, DPP_SHR + 2, 0xf, 0xf, true);
+    upto += __builtin_amdgcn_update_dpp(0, upto, DPP_SHR + 4, 0xf, 0xf, true);
+    const int nblk = __builtin_amdgcn_readlane(upto, NS - 1);
+    // block blk < nblk of the tile's streams: its stream, and one past its newest entry
     const auto block_at = [&](int blk, int &s, int &hi) {
-        s = 0, hi = 1;
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            const int n = tape_len(i), nb = (n + 15) >> 4;
-            if (blk >= 0 && blk < nb)
-                s = i, hi = n - 16 * blk;
-            blk -= nb;
-        }
+        s = __builtin_ctzll(__ballot(lane < NS && blk < upto));
+        hi = tape_len(s) - 16 * (blk - __builtin_amdgcn_readlane(upto - nb_s, s));
     };
 
     // ---- loads of the front end: a thread takes two adjacent channels of every token --------
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
     const int fe = sec == 0 ? fc : sec == 1 ? fc - DK : fc - 2 * DK;
     const int64_t fcol = sec == 2 ? (int64_t)head * DV + fe : (int64_t)hq * DK + fe;
     const int64_t ch = (sec == 0 ? 0 : (int64_t)sec * Hqk * DK) + fcol;
-    typename P::raw raw[TOK], old[TOK][W > 0 ? W : 1];
+    typename P::raw raw[TOK], old[TOK][W > 0 ? W : 1];  // old: the window at a stream's first token
     float2 w[K > 0 ? K : 1];
     if (tid < CP) {
         const T *src = (const T *)(sec == 0 ? a.q : sec == 1 ? a.k : a.v) + row0 * a.ld + fcol;
@@ -231,47 +233,56 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
 #pragma unroll
             for (int i = 0; i < K; ++i)
                 w[i] = float2{a.conv_w[ch * K + i], a.conv_w[(ch + 1) * K + i]};
-            int s = 0, t = 0;
+            const T *win = (const T *)a.conv_state_ptrs[pfx] + ch * W;
+            const T *tr = (const T *)a.tape.raw + (int64_t)b0 * cap * cd + ch;
+            const auto load_window = [&](int s, typename P::raw (&o)[W]) {
+                const int n = tape_len(s);
+                if (n >= W) {  // all on the tape
 #pragma unroll
-            for (int tok = 0; tok < TOK; ++tok) {
+                    for (int i = 0; i < W; ++i)
+                        o[i] = *(const typename P::raw *)(tr + ((int64_t)s * cap + n - W + i) * cd);
+                } else {
 #pragma unroll
-                for (int i = 0; i < W; ++i)
-                    old[tok][i] = typename P::raw{};
-                if (tok < nt) {
-                    if (t == 0) {
-                        const int n = tape_len(s);
-#pragma unroll
-                        for (int i = 0; i < W; ++i) {
-                            const int m = n - W + i;  // the tape entry, or before it the window
-                            if (n >= 0 && m >= 0)
-                                old[tok][i] = *(const typename P::raw *)((const T *)a.tape.raw +
-                                                                          ((int64_t)(b0 + s) * cap + m) * cd + ch);
-                            else if (n >= 0) {
-                                const T *ws = (const T *)a.conv_state_ptrs[pfx] + ch * W + W + m;
-                                old[tok][i] = P::make(ws, ws + W);
-                            }
-                        }
+                    for (int i = 0; i < W; ++i) {
+                        const int m = n - W + i;
+                        const bool tape = m >= 0;
+                        const T *x = tape ? tr + ((int64_t)s * cap + m) * cd : win + (n < 0 ? i : W + m);
+                        o[i] = P::make(x, x + (tape ? 1 : W));
                     }
-                    if (++t == Tn)
+                }
+            };
+            load_window(0, old[0]);
+            if (ns > 1) {
+                int s = 1, t = 1;
+#pragma unroll
+                for (int tok = 1; tok < TOK; ++tok) {
+                    if (t == Tn) {
+                        if (s < ns)
+                            load_window(s, old[tok]);
                         t = 0, ++s;
+                    }
+                    ++t;
                 }
             }
         }
     }
+    // log-gates and betas of the new tokens
+    float bet_r = 0.f, g_r = 0.f;
     if (tid >= THREADS - TOK && tid < THREADS - TOK + nt) {
         const int tok = tid - (THREADS - TOK);
-        bet[tok] = a.beta[(row0 + tok) * H + head];
+        bet_r = a.beta[(row0 + tok) * H + head];
         if constexpr (!KDA)
-            gnew[tok] = a.g[(row0 + tok) * H + head];
+            g_r = a.g[(row0 + tok) * H + head];
     }
+    constexpr int GL = KDA ? (TOK * DK / 4 + THREADS - 1) / THREADS : 1;
+    f32x4 g4r[GL];
     if constexpr (KDA) {
-        for (int i = tid; i < nt * (DK / 4); i += THREADS) {
-            const int tok = i / (DK / 4), c = 4 * (i % (DK / 4));
-            *(f32x4 *)(gk + tok * DK + c) = load4(a.g + ((row0 + tok) * H + head) * DK + c);
+#pragma unroll
+        for (int p = 0; p < GL; ++p) {
+            const int i = tid + p * THREADS, tok = i / (DK / 4), c = 4 * (i % (DK / 4));
+            g4r[p] = tok < nt ? load4(a.g + ((row0 + tok) * H + head) * DK + c) : zero4();
         }
     }
-    for (int i = tid; i < NS * GW; i += THREADS)
-        run[i] = 0.f;
 
     // ---- loads of the first tape blocks: a wave's keys and log-gates, a thread's updates ----
     f32x4 kf[DK / 16], ge[KDA ? DK / 16 : 1];
@@ -299,7 +310,7 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
         const float *dp = a.tape.d + (((int64_t)(b0 + s) * cap + hi - 1) * H + head) * DV + col;
 #pragma unroll
         for (int i = 0; i < EG; ++i) {
-            const int e = grp * EG + i;
+            const int e = grp * EG + i;  // the block's e-th newest entry
             d[i] = e < hi ? dp[-(int64_t)e * H * DV] : 0.f;
         }
     };
@@ -312,17 +323,33 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
             load_updates(p, dx[p]);
 
     // ---- front end ---------------------------------------------------------------------------
+    if (tid >= THREADS - TOK) {
+        bet[tid - (THREADS - TOK)] = bet_r;
+        gnew[tid - (THREADS - TOK)] = g_r;
+    }
+    if constexpr (KDA) {
+#pragma unroll
+        for (int p = 0; p < GL; ++p)
+            if (tid + p * THREADS < TOK * DK / 4)
+                *(f32x4 *)(gk + 4 * (tid + p * THREADS)) = g4r[p];
+    }
+    for (int i = tid; i < NS * GW; i += THREADS)
+        run[i] = 0.f;
     if (tid < CP) {
         float *dst = sec == 2 ? vd + fe : kq + (sec == 0 ? TOK * LDK : 0) + fe;
         const int ldd = sec == 2 ? DV : LDK;
         float2 win[W > 0 ? W : 1];
-        int s = 0, t = 0, n = 0;
+        T *put = nullptr;
+        int s = 0, t = 0;
 #pragma unroll
         for (int tok = 0; tok < TOK; ++tok) {
             float x0 = P::lo(raw[tok]), x1 = P::hi(raw[tok]);
             if (K > 0 && tok < nt) {
                 if (t == 0) {
-                    n = tape_len(s);
+                    const int n = tape_len(s);
+                    put = n >= 0 && (sec == 2 || own_qk)
+                              ? (T *)a.tape.raw + ((int64_t)(b0 + s) * cap + n) * cd + ch
+                              : nullptr;
 #pragma unroll
                     for (int i = 0; i < W; ++i)
                         win[i] = float2{P::lo(old[tok][i]), P::hi(old[tok][i])};
@@ -336,8 +363,8 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
                     win[i] = win[i + 1];
                 win[W > 0 ? W - 1 : 0] = float2{x0, x1};
                 x0 = silu(a0), x1 = silu(a1);
-                if (n >= 0 && (sec == 2 || own_qk))
-                    *(typename P::raw *)((T *)a.tape.raw + ((int64_t)(b0 + s) * cap + n + t) * cd + ch) = raw[tok];
+                if (put)
+                    *(typename P::raw *)(put + t * cd) = raw[tok];
                 if (++t == Tn)
                     t = 0, ++s;
             }
@@ -417,7 +444,7 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
         for (int idx = tid >> 4; idx < ns * per; idx += THREADS / 16) {
             const int s = idx * inv_p >> 16, r = idx - s * per, xx = r * inv_x >> 16, yy = r - xx * Tn;
             const int tok = s * Tn + (yy < xx ? xx : yy), j = s * Tn + (yy < xx ? yy : xx);
-            const int m = (yy < xx ? 0 : TOK) + tok;
+            const int u = yy < xx ? xx : yy, m = (yy < xx ? 0 : TOK) + tok;
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < DK / 64; ++i) {
@@ -433,7 +460,7 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
             if constexpr (!KDA)
                 sum *= __expf(gam[tok] - gam[j]);
             if (l == 0)
-                co[m * TOK + j] = sum;
+                co[((yy < xx ? 0 : TOK) + j) * TOK + u] = sum;  // by entry j, then token u
         }
     }
     if constexpr (KDA) {  // keys and queries take the decay through their token
@@ -459,6 +486,8 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
         const bool act = blk0 + wave < nblk;
         if (!EARLY && act)
             load_keys(blk0 + wave);
+        if (lane == 0)
+            sblk[wave] = act ? ws : -1;
         if (act) {  // log-decay over the block's newer entries, and over the whole block
             const bool in = whi - 1 - c16 >= 0;
             if constexpr (KDA) {
@@ -485,6 +514,7 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
             // the waves before this one with newer blocks of its stream
             int newer = (tape_len(ws) - whi) >> 4;
             newer = newer < wave ? newer : wave;
+            const bool in = whi - 1 - c16 >= 0;
             f32x4 sc[MT];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -522,19 +552,28 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
                     float f = 1.f;
                     if constexpr (!KDA)
                         f = __expf(gam[tok < nt ? tok : 0] + gs);
-                    sp[(wave * R + m) * S::LDS_ + c16] = sc[mt][r] * f;
+                    sp[(wave * R + m) * S::LDS_ + c16] = in ? sc[mt][r] * f : 0.f;
                 }
         }
         __syncthreads();
         if (EARLY && blk0 + WAVES + wave < nblk)
             load_keys(blk0 + WAVES + wave);
         // the log-decay over the blocks so far, for the next round and the state
-        if (tid < GW) {
-            for (int v = 0; v < WAVES && blk0 + v < nblk; ++v) {
-                int s, hi;
-                block_at(blk0 + v, s, hi);
-                run[s * GW + tid] += bt[v * GW + tid];
+        if constexpr (KDA) {
+            if (tid < DK) {
+                float add[WAVES];
+#pragma unroll
+                for (int v = 0; v < WAVES; ++v)
+                    add[v] = bt[v * DK + tid];
+                for (int v = 0; v < WAVES && blk0 + v < nblk; ++v)
+                    run[sblk[v] * DK + tid] += add[v];
             }
+        } else if (tid < NS) {
+            float sum = run[tid];
+#pragma unroll
+            for (int v = 0; v < WAVES; ++v)
+                sum += sblk[v] == tid ? bt[v] : 0.f;
+            run[tid] = sum;
         }
         for (int v0 = 0; v0 < WAVES && blk0 + v0 < nblk; v0 += 2) {
             if (blk0 + v0 > 0) {
@@ -551,8 +590,6 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
                 block_at(blk0 + v0 + p, s, hi);
                 const int lo = s * Tn, up = lo + Tn;
                 const float *xp = sp + (v0 + p) * R * S::LDS_ + grp * EG;
-                // scores of entries before the tape's first are of no meaning
-                const int ne = hi - grp * EG;
 #pragma unroll
                 for (int m = 0; m < TOK; ++m) {
                     if (m < lo || m >= up)
@@ -562,8 +599,8 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
                         const f32x4 xk = load4(xp + m * S::LDS_ + i), xq = load4(xp + (TOK + m) * S::LDS_ + i);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            hist[m] += i + j < ne ? xk[j] * dx[p][i + j] : 0.f;
-                            hist[TOK + m] += i + j < ne ? xq[j] * dx[p][i + j] : 0.f;
+                            hist[m] += xk[j] * dx[p][i + j];
+                            hist[TOK + m] += xq[j] * dx[p][i + j];
                         }
                     }
                 }
@@ -637,36 +674,42 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
 
     // ---- the new tokens in order, a thread per column ------------------------------------
     for (int s = grp; s < ns; s += S::G) {
-        if (slen[s] < 0)
+        const int n = tape_len(s);
+        if (n < 0)
             continue;
         const int lo = s * Tn;
-        float yk[TOK], yq[TOK];
+        float yk[TOK], yq[TOK], v[TOK], bb[TOK];
 #pragma unroll
         for (int t = 0; t < TOK; ++t) {
-            if (t >= Tn)
-                break;
-            yk[t] = 0.f, yq[t] = 0.f;
+            const int tok = lo + (t < Tn ? t : 0);  // rows past the stream's: of no use
+            yk[t] = y[tok * DV + col], yq[t] = y[(TOK + tok) * DV + col];
 #pragma unroll
-            for (int p = 0; p < S::RS; ++p) {
-                yk[t] += y[(p * R + lo + t) * DV + col];
-                yq[t] += y[(p * R + TOK + lo + t) * DV + col];
+            for (int p = 1; p < S::RS; ++p) {
+                yk[t] += y[(p * R + tok) * DV + col];
+                yq[t] += y[(p * R + TOK + tok) * DV + col];
             }
+            v[t] = vd[tok * DV + col];
+            bb[t] = bet[tok];
         }
-        float *dp = a.tape.d + (((int64_t)(b0 + s) * cap + slen[s]) * H + head) * DV + col;
+        float *dp = a.tape.d + (((int64_t)(b0 + s) * cap + n) * H + head) * DV + col;
         float *op = a.o + ((row0 + lo) * H + head) * DV + col;
 #pragma unroll
         for (int t = 0; t < TOK; ++t) {
             if (t >= Tn)
-                break;
-            const float d = bet[lo + t] * (vd[(lo + t) * DV + col] - yk[t]);
+                continue;
+            f32x4 ck[TOK / 4], cq[TOK / 4];
+#pragma unroll
+            for (int u = 0; u < TOK / 4; ++u) {
+                ck[u] = load4(co + (lo + t) * TOK + 4 * u);
+                cq[u] = load4(co + (TOK + lo + t) * TOK + 4 * u);
+            }
+            const float d = bb[t] * (v[t] - yk[t]);
             dp[(int64_t)t * H * DV] = d;
 #pragma unroll
-            for (int u = t; u < TOK; ++u) {
-                if (u >= Tn)
-                    break;
+            for (int u = t; u < TOK; ++u) {  // coefficients of tokens past T: of no use
                 if (u > t)
-                    yk[u] += co[(lo + u) * TOK + lo + t] * d;
-                yq[u] += co[(TOK + lo + u) * TOK + lo + t] * d;
+                    yk[u] += ck[u / 4][u % 4] * d;
+                yq[u] += cq[u / 4][u % 4] * d;
             }
             if (a.z)
                 y[(TOK + lo + t) * DV + col] = yq[t];
@@ -833,7 +876,7 @@ hipError_t draft_k(const DraftArgs &a, hipStream_t s)
     using S = DraftShape<DK, DV, KDA, TOK>;
     const int ns = TOK / a.T < S::NS ? TOK / a.T : S::NS;
     const int ntile = (a.share + ns - 1) / ns;
-    const int64_t grid = (int64_t)(a.B / a.share) * a.H * ntile;
+    const int64_t grid = ((int64_t)(a.B / a.share) * a.H + 7) / 8 * 8 * ntile;
     if (grid > (int64_t)INT32_MAX)
         return hipErrorInvalidValue;
     const dim3 g((unsigned)grid), t(THREADS);
