@@ -950,19 +950,17 @@ int fold(const gdn_params *p, int kda, const float *const *h_ptrs,
     return GDN_OK;
 }
 
-// The parts a row of weights is cut into: parts of at least 4096 (one workgroup's worth of
-// loads) and at most 64 of them (one wave finds the part that holds the next token).
-constexpr int32_t kVerifySeg = 4096, kVerifyParts = 64, kVerifyMaxT = 1024;
+// The parts a row of weights is cut into: multiples of 8192 elements (four rounds of loads
+// of a workgroup's 4 waves) and at most 64 of them.
+constexpr int32_t kVerifySeg = 8192, kVerifyParts = 64, kVerifyMaxT = 1024, kVerifyMaxV = 1 << 30;
 
 bool verify_shape(int32_t B, int32_t T, int32_t V, int32_t *nseg, int32_t *seg)
 {
-    if (B < 1 || T < 0 || T > kVerifyMaxT || V < 1 ||
+    if (B < 1 || T < 0 || T > kVerifyMaxT || V < 1 || V > kVerifyMaxV ||
         (int64_t)B * kVerifyParts > (int64_t)INT32_MAX)
         return false;
     int64_t s = ((int64_t)V + kVerifyParts - 1) / kVerifyParts;
     s = (s + kVerifySeg - 1) / kVerifySeg * kVerifySeg;
-    if (s > INT32_MAX)
-        return false;
     *seg = (int32_t)s;
     *nseg = (int32_t)(((int64_t)V + s - 1) / s);
     return true;
@@ -1010,7 +1008,7 @@ size_t gdn_verify_workspace_bytes(int32_t B, int32_t T, int32_t V)
     int32_t nseg = 0, seg = 0;
     if (!verify_shape(B, T, V, &nseg, &seg))
         return 0;
-    return align_up((size_t)B * nseg * 2 * sizeof(double));
+    return align_up((size_t)B * nseg * sizeof(double)) + align_up((size_t)B * 2 * sizeof(int32_t));
 }
 
 int gdn_verify(const void *target, int64_t ld_target, const void *draft_p, int64_t ld_draft,
@@ -1038,6 +1036,7 @@ int gdn_verify(const void *target, int64_t ld_target, const void *draft_p, int64
     a.B = B, a.T = T, a.V = V;
     a.accepted = accepted, a.next = next, a.len = len;
     a.part = (double *)ws;
+    a.info = (int32_t *)((char *)ws + align_up((size_t)B * a.nseg * sizeof(double)));
     return gdn::launch_verify(dtype, a, (hipStream_t)stream) == hipSuccess ? GDN_OK : GDN_E_HIP;
 }
 

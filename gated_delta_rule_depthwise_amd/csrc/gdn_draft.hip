@@ -28,6 +28,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int THREADS = 256;
 constexpr int WAVES = THREADS / 64;
+#ifndef FOLD_SL
+#define FOLD_SL 64
+#endif
 
 __device__ __forceinline__ f32x4 load_nt4(const float *p)
 {
@@ -739,18 +742,25 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
     }
 }
 
-// One workgroup: one stream and head. The state is held in MFMA accumulator layout: lane
-// (g4, c16) has rows 16*rt + 4*g4 + r and 4 adjacent columns of the wave's 64.
-template <typename T, int DK, int DV, bool KDA>
+// One workgroup: SL columns of one stream and head's state, held in MFMA accumulator layout:
+// lane (g4, c16) has rows 16*rt + 4*g4 + r and 4 adjacent columns of the wave's 64. The sum
+// over the tape starts from the state after the whole tape's decay, so that is found first;
+// the entries are taken in blocks of 16, newest first, and the log-decay after an entry is
+// summed in that order (no differences of long sums).
+template <typename T, int DK, int DV, bool KDA, int SL>
 __global__ void __launch_bounds__(THREADS) fold_kernel(const FoldArgs a)
 {
-    constexpr int CG = DV / 64, RS = WAVES / CG, RW = DK / RS, RT = RW / 16;
-    constexpr int EB = 16;  // tape entries per round
-    __shared__ __align__(16) float sf[KDA ? EB * DK : EB];  // decay after each entry
-    __shared__ __align__(16) float through[KDA ? DK : 1];   // e^{tape's total}
+    constexpr int CG = SL / 64, RS = WAVES / CG, RW = DK / RS, RT = RW / 16;
+    constexpr int EB = 16;                              // tape entries per block
+    constexpr int GW = KDA ? DK : 1;                    // log-gates per entry
+    constexpr int GP = KDA ? THREADS / DK : 1;          // threads per log-gate column
+    static_assert(RT >= 1 && EB % GP == 0, "tile map");
+    __shared__ __align__(16) float sf[EB * GW];         // decay after each entry
+    __shared__ __align__(16) float through[GW];         // decay of the whole tape
 
     const int H = a.H, Hqk = a.Hqk, cap = a.tape.cap;
-    const int b = blockIdx.x / H, head = blockIdx.x % H, pfx = b / a.share;
+    const int bh = blockIdx.x / (DV / SL), slice = blockIdx.x % (DV / SL);
+    const int b = bh / H, head = bh % H, pfx = b / a.share;
     const int rep = H / Hqk, hq = head / rep;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int c16 = lane & 15, g4 = lane >> 4;
@@ -758,7 +768,7 @@ __global__ void __launch_bounds__(THREADS) fold_kernel(const FoldArgs a)
     const int n = a.tape.len[b];
     const bool bad = n < 0 || n > cap;
     const bool on = !bad && n >= a.min_len;
-    if (head == 0 && tid == 0) {
+    if (head == 0 && slice == 0 && tid == 0) {
         if (bad && a.dbg)
             atomicOr(a.dbg, GDN_BAD_TAPE);
         if (a.len_out && a.len_out != a.tape.len)
@@ -767,7 +777,41 @@ __global__ void __launch_bounds__(THREADS) fold_kernel(const FoldArgs a)
     if (!on)
         return;
 
-    const int64_t hoff = (int64_t)head * DK * DV + (int64_t)(rs * RW + 4 * g4) * DV + 64 * cg + 4 * c16;
+    const int64_t e0 = (int64_t)b * cap;
+    const int last = n > 0 ? (n - 1) / EB * EB : 0;      // the newest block's first entry
+    // the newest block's log-gates: all threads of a column have all 16
+    const int gc = tid % GW, gp = tid / GW;
+    const float *gp0 = a.tape.g + (e0 * H + head) * GW + gc;
+    const int64_t ge = (int64_t)H * GW;
+    float gv[EB];
+    const auto load_gates = [&](int eb) {
+#pragma unroll
+        for (int e = 0; e < EB; ++e)
+            gv[e] = eb + e < n ? gp0[(eb + e) * ge] : 0.f;
+    };
+    if (gp < GP)
+        load_gates(last);
+    // and its updates and keys: lane g4 takes entries g4, 4 + g4, ...
+    f32x4 dv[EB / 4];
+    float kv[EB / 4][RT];
+    const auto load_entries = [&](int eb) {
+#pragma unroll
+        for (int q = 0; q < EB / 4; ++q) {
+            const int e = eb + 4 * q + g4;
+            const bool in = e < n;
+            const int64_t at = e0 + (in ? e : 0);
+            const f32x4 d = load4(a.tape.d + (at * H + head) * DV + SL * slice + 64 * cg + 4 * c16);
+            dv[q] = in ? d : zero4();
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const float k = a.tape.k[(at * Hqk + hq) * DK + rs * RW + 16 * rt + c16];
+                kv[q][rt] = in ? k : 0.f;
+            }
+        }
+    };
+    load_entries(last);
+    const int64_t hoff = (int64_t)head * DK * DV + (int64_t)(rs * RW + 4 * g4) * DV + SL * slice +
+                         64 * cg + 4 * c16;
     const float *hp = a.h_ptrs[pfx] + hoff;
     f32x4 hr[RT][4];
 #pragma unroll
@@ -778,7 +822,7 @@ __global__ void __launch_bounds__(THREADS) fold_kernel(const FoldArgs a)
 
     // the windows after the tape: the last K-1 raw inputs of the channels of this head (those
     // of a q/k head by its first value head)
-    if (a.K > 0) {
+    if (a.K > 0 && slice == 0) {
         const int W = a.K - 1;
         const int64_t cd = 2 * (int64_t)Hqk * DK + (int64_t)H * DV;
         const T *in = (const T *)a.conv_state_ptrs[pfx];
@@ -790,76 +834,80 @@ __global__ void __launch_bounds__(THREADS) fold_kernel(const FoldArgs a)
                                : c < 2 * DK ? (int64_t)(Hqk + hq) * DK + c - DK
                                             : 2 * (int64_t)Hqk * DK + (int64_t)head * DV + c - 2 * DK;
             T w[3];
+#pragma unroll
             for (int i = 0; i < 3; ++i) {
                 const int m = n - W + i;
                 if (i < W)
-                    w[i] = m >= 0 ? ((const T *)a.tape.raw)[((int64_t)b * cap + m) * cd + ch]
-                                  : in[ch * W + W + m];
+                    w[i] = m >= 0 ? ((const T *)a.tape.raw)[(e0 + m) * cd + ch] : in[ch * W + W + m];
             }
+#pragma unroll
             for (int i = 0; i < 3; ++i)
                 if (i < W)
                     out[ch * W + i] = w[i];
         }
     }
 
-    f32x4 acc[RT][4];
+    // the log-decay of the whole tape
+    if (gp < GP) {
+        float all = 0.f;
+        for (int eb = last;; eb -= EB) {
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc[rt][j] = zero4();
-    const int64_t e0 = (int64_t)b * cap;
-    float run = 0.f;
-    for (int eb = (n - 1) / EB * EB; eb >= 0 && n > 0; eb -= EB) {
-        const int ne = n - eb < EB ? n - eb : EB;
-        __syncthreads();
-        if constexpr (KDA) {
-            if (tid < DK)
-                for (int e = ne - 1; e >= 0; --e) {
-                    sf[e * DK + tid] = __expf(run);
-                    run += a.tape.g[((e0 + eb + e) * H + head) * DK + tid];
-                }
-        } else if (tid == 0) {
-            for (int e = ne - 1; e >= 0; --e) {
-                sf[e] = __expf(run);
-                run += a.tape.g[(e0 + eb + e) * H + head];
-            }
+            for (int e = EB - 1; e >= 0; --e)
+                all += gv[e];
+            if (eb == 0)
+                break;
+            load_gates(eb - EB);
         }
-        __syncthreads();
-        for (int q = 0; q < EB; q += 4) {
-            const int e = q + g4;
-            f32x4 dv = zero4();
-            float kv[RT];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-                kv[rt] = 0.f;
-            if (e < ne) {
-                dv = load4(a.tape.d + ((e0 + eb + e) * H + head) * DV + 64 * cg + 4 * c16);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const int c = rs * RW + 16 * rt + c16;
-                    kv[rt] = a.tape.k[((e0 + eb + e) * Hqk + hq) * DK + c] * (KDA ? sf[e * DK + c] : sf[e]);
-                }
-            }
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[rt][j] = mfma4(kv[rt], dv[j], acc[rt][j]);
-        }
+        if (gp == 0)
+            through[gc] = __expf(all);
+        if (last > 0)
+            load_gates(last);
     }
-    if (tid < (KDA ? DK : 1))
-        through[tid] = __expf(run);
     __syncthreads();
-    float *op = a.h_out_ptrs[b] + hoff;
+    f32x4 acc[RT][4];  // [row tile][column of 4]: rows r
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const float f = through[KDA ? rs * RW + 16 * rt + 4 * g4 + r : 0];
-            const f32x4 v = hr[rt][r] * f + f32x4{acc[rt][0][r], acc[rt][1][r], acc[rt][2][r], acc[rt][3][r]};
-            __builtin_nontemporal_store(v, (f32x4 *)(op + (int64_t)(16 * rt + r) * DV));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[rt][j][r] = hr[rt][r][j] * f;
         }
+    float run = 0.f;
+    for (int eb = last;; eb -= EB) {
+        if (gp < GP) {
+#pragma unroll
+            for (int e = EB - 1; e >= 0; --e) {
+                if (e % GP == gp)
+                    sf[e * GW + gc] = __expf(run);
+                run += gv[e];
+            }
+            if (eb > 0)
+                load_gates(eb - EB);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < EB / 4; ++q)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const float k = kv[q][rt] * sf[(4 * q + g4) * GW + (KDA ? rs * RW + 16 * rt + c16 : 0)];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[rt][j] = mfma4(k, dv[q][j], acc[rt][j]);
+            }
+        if (eb == 0)
+            break;
+        load_entries(eb - EB);
+        __syncthreads();
+    }
+    float *op = a.h_out_ptrs[b] + hoff;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            __builtin_nontemporal_store(f32x4{acc[rt][0][r], acc[rt][1][r], acc[rt][2][r], acc[rt][3][r]},
+                                        (f32x4 *)(op + (int64_t)(16 * rt + r) * DV));
 }
 
 // tape lengths after a fold that was asked to clear them in place
@@ -897,7 +945,11 @@ template <typename T, int DK, int DV, bool KDA> hipError_t draft_t(const DraftAr
 
 template <typename T, int DK, int DV, bool KDA> hipError_t fold_t(const FoldArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((fold_kernel<T, DK, DV, KDA>), dim3((unsigned)((int64_t)a.B * a.H)), dim3(THREADS), 0, s, a);
+    constexpr int SL = DV < FOLD_SL ? DV : FOLD_SL;
+    const int64_t grid = (int64_t)a.B * a.H * (DV / SL);
+    if (grid > (int64_t)INT32_MAX)
+        return hipErrorInvalidValue;
+    hipLaunchKernelGGL((fold_kernel<T, DK, DV, KDA, SL>), dim3((unsigned)grid), dim3(THREADS), 0, s, a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
     if (a.len_out == a.tape.len)

@@ -291,7 +291,8 @@ struct VerifyArgs {
     const float *u;
     int32_t B, T, V;
     int32_t *accepted, *next, *len;
-    double *part;                    // [B][nseg][2]: sums of max(p - q, 0) and of p
+    double *part;                    // [B][nseg]: sums of the weights
+    int32_t *info;                   // [B][2]: drafts accepted, drafts
     int32_t nseg, seg;
 };
 

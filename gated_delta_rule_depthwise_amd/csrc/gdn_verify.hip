@@ -4,10 +4,11 @@
 // Speculative sampling: draft t is accepted while u_t q_t(d_t) < p_t(d_t); with a drafts
 // accepted, the next token is drawn from r = max(p_a - q_a, 0) (p_a when none was refused) by
 // inverting its running sum at u_T * sum(r). The call reads one row of p, and one of q where
-// a draft was refused, and is bound by HBM for a batch and by latency for one stream. A row
-// is cut into parts that workgroups sum side by side (verify_sum_kernel, which finds a by
-// itself from the 2 T probabilities concerned); verify_pick_kernel finds the part that holds
-// the next token from those sums and looks through that part alone. Sums are held in float64, in
+// a draft was refused: a batch is bound by HBM, one stream by latency. One workgroup of 16
+// waves per stream sums the row, a stretch per wave, and then narrows down: the stretch that
+// holds the token is cut into 16 again (it comes from L2 now) until one wave can look at it
+// element by element. Where a few streams have long rows (launch_verify), workgroups sum parts
+// of the rows side by side first (verify_sum_kernel). Sums are held in float64 and taken in
 // a fixed order, so the token depends on nothing but the inputs.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -20,23 +21,58 @@ namespace {
 
 typedef __bf16 bf16;
 
-constexpr int THREADS = 256;
+constexpr int PICK_THREADS = 1024, PICK_WAVES = PICK_THREADS / 64;
+constexpr int SUM_THREADS = 256;
+constexpr int VE = 8;              // adjacent elements per lane and step
+constexpr int STEP = 64 * VE;      // elements per wave and step
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(bf16 x) { return (float)x; }
 
-struct Row {
-    int accepted;     // a
-    int refused;      // 1: draft a was refused, its proposal's row applies
-    int token;        // that draft
+// 8 adjacent elements from any element address: rows need no more alignment than that, and
+// the hardware takes 16-byte loads at any address
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+struct Eight {
+    float x[VE];
 };
 
-// The drafts accepted of stream b: all threads of the workgroup look at the tests side by
-// side, the first that fails is the lowest set bit of some ballot.
-template <typename T>
-__device__ Row accept(const VerifyArgs &a, int b, int *first)
+__device__ __forceinline__ Eight load8(const bf16 *p)
 {
-    int n = a.num_drafts ? a.num_drafts[b] : a.T;
+    const u32x4_any u = *(const u32x4_any *)p;
+    Eight r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r.x[2 * i] = __uint_as_float(u[i] << 16);
+        r.x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+    return r;
+}
+
+__device__ __forceinline__ Eight load8(const float *p)
+{
+    const f32x4_any a = *(const f32x4_any *)p, b = *(const f32x4_any *)(p + 4);
+    return Eight{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+}
+
+template <typename T> __device__ __forceinline__ Eight load8(const T *p, int n)
+{
+    if (n >= VE)
+        return load8(p);
+    Eight r;
+#pragma unroll
+    for (int i = 0; i < VE; ++i)
+        r.x[i] = i < n ? to_float(p[i]) : 0.f;
+    return r;
+}
+
+// The drafts accepted of stream b, and the number of its drafts: the workgroup's threads look
+// at the tests side by side; the first that fails counts.
+template <typename T, int THREADS>
+__device__ int accept(const VerifyArgs &a, int b, int *first, int &n)
+{
+    n = a.num_drafts ? a.num_drafts[b] : a.T;
     n = n < 0 ? 0 : n > a.T ? a.T : n;
     if (threadIdx.x == 0)
         *first = n;
@@ -47,158 +83,237 @@ __device__ Row accept(const VerifyArgs &a, int b, int *first)
         if (tok >= 0 && tok < a.V) {
             const double p = to_float(((const T *)a.target)[((int64_t)b * (a.T + 1) + t) * a.ld_target + tok]);
             const double q = a.draft ? to_float(((const T *)a.draft)[((int64_t)b * a.T + t) * a.ld_draft + tok]) : 1.f;
-            ok = (double)a.u[(int64_t)b * (a.T + 1) + t] * q < p;  // exact: 24 + 24 bits
+            ok = (double)a.u[(int64_t)b * (a.T + 1) + t] * q < p;  // the product is exact: 24 + 24 bits
         }
         if (!ok)
             atomicMin(first, t);
     }
     __syncthreads();
-    const int k = *first;
-    return Row{k, k < n, k < n ? a.tokens[(int64_t)b * a.T + k] : -1};
+    return *first;
 }
 
-// weights of element v: r = max(p - q, 0) and p; NaN and negative values count as zero
+// The weights r = max(p - q, 0) of a stream's next token; NaN and negative values count as
+// zero. q: the refused draft's proposal (nullptr: none, or 1 at token one_hot alone).
 template <typename T> struct Weights {
     const T *p, *q;
-    int one_hot;  // token whose proposal is 1 (draft == nullptr), or -1
-    __device__ Weights(const VerifyArgs &a, int b, const Row &r)
+    int one_hot;
+    __device__ Weights(const VerifyArgs &a, int b, int accepted, int n)
     {
-        p = (const T *)a.target + ((int64_t)b * (a.T + 1) + r.accepted) * a.ld_target;
-        q = r.refused && a.draft ? (const T *)a.draft + ((int64_t)b * a.T + r.accepted) * a.ld_draft : nullptr;
-        one_hot = r.refused && !a.draft ? r.token : -1;
+        const bool refused = accepted < n;
+        p = (const T *)a.target + ((int64_t)b * (a.T + 1) + accepted) * a.ld_target;
+        q = refused && a.draft ? (const T *)a.draft + ((int64_t)b * a.T + accepted) * a.ld_draft : nullptr;
+        one_hot = refused && !a.draft ? a.tokens[(int64_t)b * a.T + accepted] : -1;
     }
-    __device__ float plain(int v) const { return fmaxf(to_float(p[v]), 0.f); }
-    __device__ float rest(int v) const
+    __device__ __forceinline__ Eight combine(int v, Eight x, const Eight &y) const
     {
-        const float x = to_float(p[v]) - (q ? to_float(q[v]) : v == one_hot ? 1.f : 0.f);
-        return fmaxf(x, 0.f);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+            const float s = q ? y.x[i] : v + i == one_hot ? 1.f : 0.f;
+            x.x[i] = fmaxf(x.x[i] - s, 0.f);
+        }
+        return x;
+    }
+    // elements v .. v+7, those at or past `hi` as 0
+    __device__ __forceinline__ Eight at(int v, int hi) const
+    {
+        const int n = hi - v;
+        return combine(v, load8(p + v, n), q ? load8(q + v, n) : Eight{});
     }
 };
 
-// sum over the workgroup, in a fixed order; every thread gets it
-__device__ double block_sum(double x, double *red)
+__device__ __forceinline__ double sum8(const Eight &e)
 {
+    double s = 0.;
+#pragma unroll
+    for (int i = 0; i < VE; ++i)
+        s += e.x[i];
+    return s;
+}
+
+// Sum of the weights of elements lo .. hi-1 over a wave; every lane gets it. Four steps'
+// loads are in flight together.
+template <typename T> __device__ double wave_sum(const Weights<T> &w, int lo, int hi)
+{
+    const int lane = threadIdx.x & 63;
+    double sum = 0.;
+    int v = lo + lane * VE;
+    if (hi - lo >= 4 * STEP) {
+        for (; v <= hi - 3 * STEP - VE; v += 4 * STEP) {
+            Eight x[4], y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[i] = load8(w.p + v + i * STEP);
+            if (w.q) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    y[i] = load8(w.q + v + i * STEP);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sum += sum8(w.combine(v + i * STEP, x[i], y[i]));
+        }
+    }
+    for (; v < hi; v += STEP)
+        sum += sum8(w.at(v, hi));
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1)
-        x += __shfl_xor(x, m);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0)
-        red[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = 0.;
-    for (int i = 0; i < THREADS / 64; ++i)
-        x += red[i];
-    return x;
+        sum += __shfl_xor(sum, m);
+    return sum;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(THREADS) verify_sum_kernel(const VerifyArgs a)
+__global__ void __launch_bounds__(SUM_THREADS) verify_sum_kernel(const VerifyArgs a)
 {
+    constexpr int WAVES = SUM_THREADS / 64;
     __shared__ int first;
-    __shared__ double red[THREADS / 64];
-    const int b = blockIdx.x / a.nseg, sg = blockIdx.x % a.nseg;
-    const Row row = accept<T>(a, b, &first);
-    const Weights<T> w(a, b, row);
+    __shared__ double red[WAVES];
+    const int b = blockIdx.x / a.nseg, sg = blockIdx.x % a.nseg, wave = threadIdx.x >> 6;
+    int n;
+    const int acc = accept<T, SUM_THREADS>(a, b, &first, n);
+    const Weights<T> w(a, b, acc, n);
+    // a part is a multiple of 4 * STEP elements, but for the row's end
     const int v0 = sg * a.seg, v1 = a.V - v0 < a.seg ? a.V : v0 + a.seg;
-    double r = 0., p = 0.;
-    for (int v = v0 + threadIdx.x; v < v1; v += THREADS) {
-        p += w.plain(v);
-        r += w.rest(v);
-    }
-    r = block_sum(r, red);
-    p = block_sum(p, red);
+    const int per = a.seg / WAVES, lo = v0 + wave * per;
+    const int hi = lo >= v1 ? lo : v1 - lo < per ? v1 : lo + per;
+    const double sum = wave_sum(w, lo, hi);
+    if ((threadIdx.x & 63) == 0)
+        red[wave] = sum;
+    __syncthreads();
     if (threadIdx.x == 0) {
-        double *out = a.part + ((int64_t)b * a.nseg + sg) * 2;
-        out[0] = r, out[1] = p;
+        double s = 0.;
+        for (int i = 0; i < WAVES; ++i)
+            s += red[i];
+        a.part[(int64_t)b * a.nseg + sg] = s;
+        if (sg == 0) {
+            a.info[2 * b] = acc;
+            a.info[2 * b + 1] = n;
+        }
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(THREADS) verify_pick_kernel(const VerifyArgs a)
+// The first of `n` sums (LDS or global) at which the running sum from `before` passes `aim`, or
+// where rounding leaves none the last that is not zero (-1: all are). before: up to it.
+__device__ __forceinline__ int find(const double *sums, int n, double aim, double &before)
+{
+    double run = before;
+    int at = -1;
+    for (int i = 0; i < n; ++i) {
+        const double x = sums[i];
+        if (x > 0.)
+            at = i, before = run;
+        run += x;
+        if (run > aim && at == i)
+            break;
+    }
+    return at;
+}
+
+template <typename T, bool PARTS>
+__global__ void __launch_bounds__(PICK_THREADS) verify_pick_kernel(const VerifyArgs a)
 {
     __shared__ int first;
-    __shared__ double cum[THREADS];
-    __shared__ int found, last;
-    const int b = blockIdx.x, tid = threadIdx.x;
-    const Row row = accept<T>(a, b, &first);
-    const Weights<T> w(a, b, row);
-    const double *part = a.part + (int64_t)b * a.nseg * 2;
-    // the part that holds the token: the first whose running sum passes the aim, or where
-    // rounding leaves none the last that holds any weight
-    double total = 0.;
-    for (int i = 0; i < a.nseg; ++i)
-        total += part[2 * i];
-    const bool use_p = !(total > 0.);
-    if (use_p) {
-        total = 0.;
-        for (int i = 0; i < a.nseg; ++i)
-            total += part[2 * i + 1];
+    __shared__ double sums[64];
+    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int acc, n, nsum = PICK_WAVES;
+    if constexpr (PARTS)
+        acc = a.info[2 * b], n = a.info[2 * b + 1];
+    else
+        acc = accept<T, PICK_THREADS>(a, b, &first, n);
+    Weights<T> w(a, b, acc, n);
+
+    // sums of the row's stretches of `per` elements, into sums[0 .. nsum)
+    int lo = 0, hi = a.V, per = 0;
+    const auto cut = [&]() {
+        per = (hi - lo + PICK_WAVES - 1) / PICK_WAVES;
+        per = (per + VE - 1) / VE * VE;
+        const int64_t at = (int64_t)lo + (int64_t)wave * per;
+        const int l = at < hi ? (int)at : hi, h = hi - l < per ? hi : l + per;
+        const double s = wave_sum(w, l, h);
+        __syncthreads();
+        if (lane == 0)
+            sums[wave] = s;
+        __syncthreads();
+    };
+    const auto total = [&]() {
+        double s = 0.;
+        for (int i = 0; i < nsum; ++i)
+            s += sums[i];
+        return s;
+    };
+    if constexpr (PARTS) {
+        if (tid < a.nseg)
+            sums[tid] = a.part[(int64_t)b * a.nseg + tid];
+        nsum = a.nseg, per = a.seg;
+        __syncthreads();
+    } else
+        cut();
+    double all = total();
+    if (!(all > 0.) && (w.q || w.one_hot >= 0)) {  // nothing is left over: draw from p itself
+        w.q = nullptr, w.one_hot = -1;
+        nsum = PICK_WAVES;
+        cut();
+        all = total();
     }
-    const double aim = (double)a.u[(int64_t)b * (a.T + 1) + a.T] * total;
-    double before = 0.;
-    int sg = -1;
-    {
-        double run = 0.;
-        for (int i = 0; i < a.nseg; ++i) {
-            const double x = part[2 * i + use_p];
-            if (x > 0.)
-                sg = i, before = run;
-            run += x;
-            if (run > aim)
+    int next = -1;
+    if (all > 0.) {
+        const double aim = (double)a.u[(int64_t)b * (a.T + 1) + a.T] * all;
+        double before = 0.;
+        for (;;) {
+            const int found = find(sums, nsum, aim, before), at = found < 0 ? 0 : found;
+            lo = lo + at * per;
+            hi = hi - lo < per ? hi : lo + per;
+            if (hi - lo <= STEP)
                 break;
+            nsum = PICK_WAVES;
+            cut();
         }
-    }
-    if (tid == 0)
-        found = 0x7fffffff, last = -1;
-    __syncthreads();
-    if (sg >= 0) {
-        // each thread a run of consecutive elements of the part
-        const int v0 = sg * a.seg, v1 = a.V - v0 < a.seg ? a.V : v0 + a.seg;
-        const int per = (v1 - v0 + THREADS - 1) / THREADS;
-        const int64_t e0 = (int64_t)v0 + (int64_t)tid * per;
-        const int lo = e0 < v1 ? (int)e0 : v1, hi = v1 - lo < per ? v1 : lo + per;
-        double sum = 0.;
-        int mine = -1;
-        for (int v = lo; v < hi; ++v) {
-            const float x = use_p ? w.plain(v) : w.rest(v);
-            sum += x;
-            if (x > 0.f)
-                mine = v;
-        }
-        cum[tid] = sum;
-        if (mine >= 0)
-            atomicMax(&last, mine);
-        __syncthreads();
-        double run = before;
-        for (int i = 0; i < tid; ++i)
-            run += cum[i];
-        if (run <= aim) {
-            for (int v = lo; v < hi; ++v) {
-                run += use_p ? w.plain(v) : w.rest(v);
-                if (run > aim) {
-                    atomicMin(&found, v);
-                    break;
-                }
+        if (wave == 0) {
+            const Eight x = w.at(lo + lane * VE, hi);
+            const double own = sum8(x);
+            double run = own;
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const double y = __shfl_up(run, m);
+                run += lane >= m ? y : 0.;
             }
-        } else if (tid > 0) {
-            // an earlier thread's run has it
+            run = before + (run - own);
+            int hit = -1, last = -1;
+#pragma unroll
+            for (int i = 0; i < VE; ++i) {
+                run += x.x[i];
+                if (x.x[i] > 0.f)
+                    last = i;
+                if (hit < 0 && x.x[i] > 0.f && run > aim)
+                    hit = i;
+            }
+            const uint64_t hits = __ballot(hit >= 0), any = __ballot(last >= 0);
+            const int l = hits ? __builtin_ctzll(hits) : any ? 63 - __builtin_clzll(any) : 0;
+            const int i = __shfl(hits ? hit : last, l);
+            next = lo + l * VE + i;
         }
-        __syncthreads();
     }
     if (tid == 0) {
-        a.accepted[b] = row.accepted;
-        a.next[b] = found != 0x7fffffff ? found : last;
+        a.accepted[b] = acc;
+        a.next[b] = next;
         if (a.len)
-            a.len[b] += row.accepted + 1;
+            a.len[b] += acc + 1;
     }
 }
 
 template <typename T> hipError_t verify_t(const VerifyArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((verify_sum_kernel<T>), dim3((unsigned)(a.B * a.nseg)), dim3(THREADS), 0, s, a);
+    // Rows of a batch that fills the device, or short ones, are one workgroup's work each;
+    // a workgroup alone draws about 100 bytes per ns, so two rows of 256 KiB cost it about
+    // as much as the second launch of the other way.
+    if (a.B >= 48 || (int64_t)a.V * (int64_t)sizeof(T) <= (256 << 10)) {
+        hipLaunchKernelGGL((verify_pick_kernel<T, false>), dim3((unsigned)a.B), dim3(PICK_THREADS), 0, s, a);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((verify_sum_kernel<T>), dim3((unsigned)(a.B * a.nseg)), dim3(SUM_THREADS), 0, s, a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
-    hipLaunchKernelGGL((verify_pick_kernel<T>), dim3((unsigned)a.B), dim3(THREADS), 0, s, a);
+    hipLaunchKernelGGL((verify_pick_kernel<T, true>), dim3((unsigned)a.B), dim3(PICK_THREADS), 0, s, a);
     return hipGetLastError();
 }
 

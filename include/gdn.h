@@ -361,8 +361,9 @@ int kda_fold(const gdn_params *p, const float *const *h_ptrs,
  *              accepted drafts and the token before them (a gdn_draft call over the T+1 rows
  *              of that token and its drafts gave the target's T+1 rows).
  *   ws         >= gdn_verify_workspace_bytes(B, T, V), 16-byte aligned.
- * 0 <= T <= 1024, V >= 1, ld >= V. Sums are held in float64; weights that are negative or NaN
- * count as zero. Only rows a of the probabilities are read whole. Two launches.
+ * 0 <= T <= 1024, 1 <= V <= 2^30, ld >= V. Sums are held in float64; weights that are negative
+ * or NaN count as zero. Only rows a of the probabilities are read whole. One launch, or two
+ * for a few streams with long rows.
  */
 int gdn_verify(const void *target, int64_t ld_target, const void *draft, int64_t ld_draft,
                int32_t dtype, const int32_t *tokens, const int32_t *num_drafts,
