@@ -28,9 +28,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int THREADS = 256;
 constexpr int WAVES = THREADS / 64;
-#ifndef FOLD_SL
-#define FOLD_SL 64
-#endif
 
 __device__ __forceinline__ f32x4 load_nt4(const float *p)
 {
@@ -144,12 +141,21 @@ template <int DK, int DV, bool KDA, int TOK> struct DraftShape {
     static constexpr int VD = RUN + NS * GW;                  // v
     static constexpr int CO = VD + TOK * DV;                  // coefficients among new tokens
     static constexpr int SM = CO + R * TOK;                   // small: see the kernel
-    static constexpr int TOTAL = SM + 3 * TOK + NS + WAVES;
+    static constexpr int TOTAL = SM + 2 * TOK + NS + WAVES;
     static_assert(RW % 16 == 0 && DK % 16 == 0, "tile map");
 };
 
+// Waves per SIMD the registers are held to: with fewer tokens and the scalar gate four
+// workgroups of a CU hide each other's waits (256 streams x 8 tokens: 174 us with 4, 188 us
+// with 3); the channel gates' factors and the wide instances would spill there (32 x 4 tokens:
+// 44 us with 3 and spills, 36 us with 2).
+template <int DK, int DV, bool KDA, int TOK> constexpr int draft_waves()
+{
+    return TOK == 16 ? 2 : DK == 64 || (!KDA && DV == 128) ? 4 : KDA ? 2 : 3;
+}
+
 template <typename T, int DK, int DV, bool KDA, int K, int TOK>
-__global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 : 2) draft_kernel(const DraftArgs a, int ntile)
+__global__ void __launch_bounds__(THREADS, (draft_waves<DK, DV, KDA, TOK>())) draft_kernel(const DraftArgs a, int ntile)
 {
     using S = DraftShape<DK, DV, KDA, TOK>;
     using P = Pair<T>;
@@ -160,8 +166,7 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
     float *const gk = sm + S::GK, *const y = sm + S::Y, *const run = sm + S::RUN;
     float *const vd = sm + S::VD, *const co = sm + S::CO;
     float *const gam = sm + S::SM;        // [TOK] log-gates through each new token (GDN)
-    float *const gnew = gam + TOK;        // [TOK] log-gates of the new tokens (GDN)
-    float *const bet = gnew + TOK;        // [TOK]
+    float *const bet = gam + TOK;         // [TOK]
     int *const slen = (int *)(bet + TOK); // [NS] tape lengths, -1: stream left out
     int *const sblk = slen + NS;          // [WAVES] the streams of a round's blocks
 
@@ -327,8 +332,26 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
 
     // ---- front end ---------------------------------------------------------------------------
     if (tid >= THREADS - TOK) {
-        bet[tid - (THREADS - TOK)] = bet_r;
-        gnew[tid - (THREADS - TOK)] = g_r;
+        const int tok = tid - (THREADS - TOK), s = stream_of(tok);
+        bet[tok] = bet_r;
+        if constexpr (!KDA) {  // the log-gates through each token, and the tape's
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < TOK; ++j) {
+                const float gj = __builtin_bit_cast(
+                    float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, g_r), 64 - TOK + j));
+                sum += j >= s * Tn && j <= tok ? gj : 0.f;
+            }
+            gam[tok] = sum;
+            int n = -1;
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {  // by readlane: the other lanes are not in here
+                const int ni = tape_len(i);
+                n = s == i ? ni : n;
+            }
+            if (tok < nt && n >= 0)
+                a.tape.g[((int64_t)(b0 + s) * cap + n + tok - s * Tn) * H + head] = g_r;
+        }
     }
     if constexpr (KDA) {
 #pragma unroll
@@ -402,13 +425,13 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
                            4 * l + 64 * i) = v[i];
         }
     }
-    // running sums of the log-gates within each stream's new tokens; their tape entries
+    // KDA: running sums of the log-gates within each stream's new tokens; their tape entries
     if constexpr (KDA) {
         if (tid < DK) {
             float gv[TOK];
 #pragma unroll
             for (int tok = 0; tok < TOK; ++tok)
-                gv[tok] = tok < nt ? gk[tok * DK + tid] : 0.f;
+                gv[tok] = gk[tok * DK + tid];
             int s = 0, t = 0, n = 0;
             float sum = 0.f;
 #pragma unroll
@@ -425,18 +448,6 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
                 }
             }
         }
-    } else if (tid < nt) {
-        const int s = stream_of(tid), n = slen[s];
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < TOK; ++j) {
-            const float gv = gnew[j];
-            if (j >= s * Tn && j <= tid)
-                sum += gv;
-        }
-        gam[tid] = sum;
-        if (n >= 0)
-            a.tape.g[((int64_t)(b0 + s) * cap + n + tid - s * Tn) * H + head] = gnew[tid];
     }
     __syncthreads();
 
@@ -743,20 +754,20 @@ __global__ void __launch_bounds__(THREADS, TOK == 8 && !(KDA && DK == 128) ? 3 :
 }
 
 // One workgroup: SL columns of one stream and head's state, held in MFMA accumulator layout:
-// lane (g4, c16) has rows 16*rt + 4*g4 + r and 4 adjacent columns of the wave's 64. The sum
-// over the tape starts from the state after the whole tape's decay, so that is found first;
-// the entries are taken in blocks of 16, newest first, and the log-decay after an entry is
-// summed in that order (no differences of long sums).
+// lane (g4, c16) has rows 16*rt + 4*g4 + r and 4 adjacent columns of the wave's 64. The tape
+// is taken in blocks of 16 entries, oldest first: the state times the block's decay, plus the
+// block's entries with the decay after each (summed from the newest back: no differences of
+// long sums). A block's loads go out while the one before is worked in.
 template <typename T, int DK, int DV, bool KDA, int SL>
-__global__ void __launch_bounds__(THREADS) fold_kernel(const FoldArgs a)
+__global__ void __launch_bounds__(THREADS, SL == 64 ? 4 : 3) fold_kernel(const FoldArgs a)
 {
     constexpr int CG = SL / 64, RS = WAVES / CG, RW = DK / RS, RT = RW / 16;
     constexpr int EB = 16;                              // tape entries per block
     constexpr int GW = KDA ? DK : 1;                    // log-gates per entry
     constexpr int GP = KDA ? THREADS / DK : 1;          // threads per log-gate column
     static_assert(RT >= 1 && EB % GP == 0, "tile map");
-    __shared__ __align__(16) float sf[EB * GW];         // decay after each entry
-    __shared__ __align__(16) float through[GW];         // decay of the whole tape
+    __shared__ __align__(16) float sf[2][EB * GW];      // decay after each entry
+    __shared__ __align__(16) float through[2][GW];      // decay of the block
 
     const int H = a.H, Hqk = a.Hqk, cap = a.tape.cap;
     const int bh = blockIdx.x / (DV / SL), slice = blockIdx.x % (DV / SL);
@@ -778,8 +789,7 @@ __global__ void __launch_bounds__(THREADS) fold_kernel(const FoldArgs a)
         return;
 
     const int64_t e0 = (int64_t)b * cap;
-    const int last = n > 0 ? (n - 1) / EB * EB : 0;      // the newest block's first entry
-    // the newest block's log-gates: all threads of a column have all 16
+    // a block's log-gates: all threads of a column have all 16
     const int gc = tid % GW, gp = tid / GW;
     const float *gp0 = a.tape.g + (e0 * H + head) * GW + gc;
     const int64_t ge = (int64_t)H * GW;
@@ -789,9 +799,7 @@ __global__ void __launch_bounds__(THREADS) fold_kernel(const FoldArgs a)
         for (int e = 0; e < EB; ++e)
             gv[e] = eb + e < n ? gp0[(eb + e) * ge] : 0.f;
     };
-    if (gp < GP)
-        load_gates(last);
-    // and its updates and keys: lane g4 takes entries g4, 4 + g4, ...
+    // its updates and keys: lane g4 takes entries g4, 4 + g4, ...
     f32x4 dv[EB / 4];
     float kv[EB / 4][RT];
     const auto load_entries = [&](int eb) {
@@ -809,16 +817,23 @@ __global__ void __launch_bounds__(THREADS) fold_kernel(const FoldArgs a)
             }
         }
     };
-    load_entries(last);
+    if (gp < GP)
+        load_gates(0);
+    load_entries(0);
     const int64_t hoff = (int64_t)head * DK * DV + (int64_t)(rs * RW + 4 * g4) * DV + SL * slice +
                          64 * cg + 4 * c16;
     const float *hp = a.h_ptrs[pfx] + hoff;
-    f32x4 hr[RT][4];
+    f32x4 acc[RT][4];  // [row tile][column of 4]: rows r
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+    for (int rt = 0; rt < RT; ++rt) {
+        f32x4 hr[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            hr[rt][r] = load_nt4(hp + (int64_t)(16 * rt + r) * DV);
+            hr[r] = load_nt4(hp + (int64_t)(16 * rt + r) * DV);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[rt][j] = f32x4{hr[0][j], hr[1][j], hr[2][j], hr[3][j]};
+    }
 
     // the windows after the tape: the last K-1 raw inputs of the channels of this head (those
     // of a q/k head by its first value head)
@@ -847,59 +862,41 @@ __global__ void __launch_bounds__(THREADS) fold_kernel(const FoldArgs a)
         }
     }
 
-    // the log-decay of the whole tape
-    if (gp < GP) {
-        float all = 0.f;
-        for (int eb = last;; eb -= EB) {
-#pragma unroll
-            for (int e = EB - 1; e >= 0; --e)
-                all += gv[e];
-            if (eb == 0)
-                break;
-            load_gates(eb - EB);
-        }
-        if (gp == 0)
-            through[gc] = __expf(all);
-        if (last > 0)
-            load_gates(last);
-    }
-    __syncthreads();
-    f32x4 acc[RT][4];  // [row tile][column of 4]: rows r
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const float f = through[KDA ? rs * RW + 16 * rt + 4 * g4 + r : 0];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[rt][j][r] = hr[rt][r][j] * f;
-        }
-    float run = 0.f;
-    for (int eb = last;; eb -= EB) {
+    for (int eb = 0, buf = 0; eb < n; eb += EB, buf ^= 1) {
         if (gp < GP) {
+            float run = 0.f;
 #pragma unroll
             for (int e = EB - 1; e >= 0; --e) {
                 if (e % GP == gp)
-                    sf[e * GW + gc] = __expf(run);
+                    sf[buf][e * GW + gc] = __expf(run);
                 run += gv[e];
             }
-            if (eb > 0)
-                load_gates(eb - EB);
+            if (gp == 0)
+                through[buf][gc] = __expf(run);
+            if (eb + EB < n)
+                load_gates(eb + EB);
         }
-        __syncthreads();
+        __syncthreads();  // one per block: its factors lie in the buffer of the one before last
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float f = through[buf][KDA ? rs * RW + 16 * rt + 4 * g4 + r : 0];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[rt][j][r] *= f;
+            }
 #pragma unroll
         for (int q = 0; q < EB / 4; ++q)
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                const float k = kv[q][rt] * sf[(4 * q + g4) * GW + (KDA ? rs * RW + 16 * rt + c16 : 0)];
+                const float k = kv[q][rt] * sf[buf][(4 * q + g4) * GW + (KDA ? rs * RW + 16 * rt + c16 : 0)];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     acc[rt][j] = mfma4(k, dv[q][j], acc[rt][j]);
             }
-        if (eb == 0)
-            break;
-        load_entries(eb - EB);
-        __syncthreads();
+        if (eb + EB < n)
+            load_entries(eb + EB);
     }
     float *op = a.h_out_ptrs[b] + hoff;
 #pragma unroll
@@ -943,9 +940,8 @@ template <typename T, int DK, int DV, bool KDA> hipError_t draft_t(const DraftAr
     return a.T <= 8 ? draft_k<T, DK, DV, KDA, 8>(a, s) : draft_k<T, DK, DV, KDA, 16>(a, s);
 }
 
-template <typename T, int DK, int DV, bool KDA> hipError_t fold_t(const FoldArgs &a, hipStream_t s)
+template <typename T, int DK, int DV, bool KDA, int SL> hipError_t fold_s(const FoldArgs &a, hipStream_t s)
 {
-    constexpr int SL = DV < FOLD_SL ? DV : FOLD_SL;
     const int64_t grid = (int64_t)a.B * a.H * (DV / SL);
     if (grid > (int64_t)INT32_MAX)
         return hipErrorInvalidValue;
@@ -956,6 +952,16 @@ template <typename T, int DK, int DV, bool KDA> hipError_t fold_t(const FoldArgs
         hipLaunchKernelGGL(fold_len_kernel, dim3((unsigned)((a.B + THREADS - 1) / THREADS)), dim3(THREADS), 0, s,
                            a.tape.len, a.B, a.tape.cap, a.min_len);
     return hipGetLastError();
+}
+
+template <typename T, int DK, int DV, bool KDA> hipError_t fold_t(const FoldArgs &a, hipStream_t s)
+{
+    // Slices of 64 columns at 4 waves per SIMD (64 x 32 heads: 57.5 us, whole rows of 128 columns
+    // 61.8 us; 1 x 32 heads: 6.4 us and 8.8 us), but for many channel-gated heads, whose factors
+    // each slice forms again (48 x 32 heads: slices 48 us, whole rows 44 us).
+    if (KDA && DV > 64 && (int64_t)a.B * a.H >= 1024)
+        return fold_s<T, DK, DV, KDA, DV < 128 ? DV : 128>(a, s);
+    return fold_s<T, DK, DV, KDA, 64>(a, s);
 }
 
 // f<T, DK, DV, KDA>(a, s) for the compiled configurations: bf16 (64, 64), (128, 128) and

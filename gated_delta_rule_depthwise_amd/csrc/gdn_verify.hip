@@ -5,11 +5,11 @@
 // accepted, the next token is drawn from r = max(p_a - q_a, 0) (p_a when none was refused) by
 // inverting its running sum at u_T * sum(r). The call reads one row of p, and one of q where
 // a draft was refused: a batch is bound by HBM, one stream by latency. One workgroup of 16
-// waves per stream sums the row, a stretch per wave, and then narrows down: the stretch that
-// holds the token is cut into 16 again (it comes from L2 now) until one wave can look at it
-// element by element. Where a few streams have long rows (launch_verify), workgroups sum parts
-// of the rows side by side first (verify_sum_kernel). Sums are held in float64 and taken in
-// a fixed order, so the token depends on nothing but the inputs.
+// waves per stream sums the row, a stretch per wave, and narrows down to at most 8192 elements
+// (which come from L2 then), 8 per thread, whose running sum gives the token. Where a few
+// streams have long rows (launch_verify), workgroups sum parts of the rows side by side first
+// (verify_sum_kernel). Sums are held in float64 and taken in a fixed order, so the token
+// depends on nothing but the inputs.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -25,6 +25,7 @@ constexpr int PICK_THREADS = 1024, PICK_WAVES = PICK_THREADS / 64;
 constexpr int SUM_THREADS = 256;
 constexpr int VE = 8;              // adjacent elements per lane and step
 constexpr int STEP = 64 * VE;      // elements per wave and step
+constexpr int LAST = PICK_THREADS * VE;  // elements looked at one by one
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(bf16 x) { return (float)x; }
@@ -34,9 +35,7 @@ __device__ __forceinline__ float to_float(bf16 x) { return (float)x; }
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
-struct Eight {
-    float x[VE];
-};
+typedef float Eight __attribute__((ext_vector_type(VE)));
 
 __device__ __forceinline__ Eight load8(const bf16 *p)
 {
@@ -44,8 +43,8 @@ __device__ __forceinline__ Eight load8(const bf16 *p)
     Eight r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        r.x[2 * i] = __uint_as_float(u[i] << 16);
-        r.x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        r[2 * i] = __uint_as_float(u[i] << 16);
+        r[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
     return r;
 }
@@ -53,43 +52,47 @@ __device__ __forceinline__ Eight load8(const bf16 *p)
 __device__ __forceinline__ Eight load8(const float *p)
 {
     const f32x4_any a = *(const f32x4_any *)p, b = *(const f32x4_any *)(p + 4);
-    return Eight{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+    return Eight{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
 template <typename T> __device__ __forceinline__ Eight load8(const T *p, int n)
 {
-    if (n >= VE)
-        return load8(p);
-    Eight r;
+    Eight r = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (n >= VE) {
+        r = load8(p);
+    } else {
 #pragma unroll
-    for (int i = 0; i < VE; ++i)
-        r.x[i] = i < n ? to_float(p[i]) : 0.f;
+        for (int i = 0; i < VE; ++i)
+            if (i < n)
+                r[i] = to_float(p[i]);
+    }
     return r;
 }
 
 // The drafts accepted of stream b, and the number of its drafts: the workgroup's threads look
 // at the tests side by side; the first that fails counts.
 template <typename T, int THREADS>
-__device__ int accept(const VerifyArgs &a, int b, int *first, int &n)
+__device__ __forceinline__ int accept(const VerifyArgs &a, int b, int *first, int &n)
 {
     n = a.num_drafts ? a.num_drafts[b] : a.T;
-    n = n < 0 ? 0 : n > a.T ? a.T : n;
     if (threadIdx.x == 0)
-        *first = n;
+        *first = a.T;
     __syncthreads();
-    for (int t = threadIdx.x; t < n; t += THREADS) {
+    for (int t = threadIdx.x; t < a.T; t += THREADS) {
         const int tok = a.tokens[(int64_t)b * a.T + t];
+        const float u = a.u[(int64_t)b * (a.T + 1) + t];
         bool ok = false;
         if (tok >= 0 && tok < a.V) {
             const double p = to_float(((const T *)a.target)[((int64_t)b * (a.T + 1) + t) * a.ld_target + tok]);
             const double q = a.draft ? to_float(((const T *)a.draft)[((int64_t)b * a.T + t) * a.ld_draft + tok]) : 1.f;
-            ok = (double)a.u[(int64_t)b * (a.T + 1) + t] * q < p;  // the product is exact: 24 + 24 bits
+            ok = (double)u * q < p;  // the product is exact: 24 + 24 bits
         }
         if (!ok)
             atomicMin(first, t);
     }
+    n = n < 0 ? 0 : n > a.T ? a.T : n;
     __syncthreads();
-    return *first;
+    return *first < n ? *first : n;
 }
 
 // The weights r = max(p - q, 0) of a stream's next token; NaN and negative values count as
@@ -104,12 +107,12 @@ template <typename T> struct Weights {
         q = refused && a.draft ? (const T *)a.draft + ((int64_t)b * a.T + accepted) * a.ld_draft : nullptr;
         one_hot = refused && !a.draft ? a.tokens[(int64_t)b * a.T + accepted] : -1;
     }
-    __device__ __forceinline__ Eight combine(int v, Eight x, const Eight &y) const
+    __device__ __forceinline__ Eight combine(int v, Eight x, Eight y) const
     {
 #pragma unroll
         for (int i = 0; i < VE; ++i) {
-            const float s = q ? y.x[i] : v + i == one_hot ? 1.f : 0.f;
-            x.x[i] = fmaxf(x.x[i] - s, 0.f);
+            const float s = q ? y[i] : v + i == one_hot ? 1.f : 0.f;
+            x[i] = fmaxf(x[i] - s, 0.f);
         }
         return x;
     }
@@ -117,44 +120,63 @@ template <typename T> struct Weights {
     __device__ __forceinline__ Eight at(int v, int hi) const
     {
         const int n = hi - v;
-        return combine(v, load8(p + v, n), q ? load8(q + v, n) : Eight{});
+        const Eight x = load8(p + v, n);
+        Eight y = x;
+        if (q)
+            y = load8(q + v, n);
+        return combine(v, x, y);
     }
 };
 
-__device__ __forceinline__ double sum8(const Eight &e)
+__device__ __forceinline__ double sum8(Eight e)
 {
     double s = 0.;
 #pragma unroll
     for (int i = 0; i < VE; ++i)
-        s += e.x[i];
+        s += e[i];
     return s;
 }
 
 // Sum of the weights of elements lo .. hi-1 over a wave; every lane gets it. Four steps'
-// loads are in flight together.
-template <typename T> __device__ double wave_sum(const Weights<T> &w, int lo, int hi)
+// loads are in flight together; the lane that holds the row's end has its own.
+template <typename T> __device__ __forceinline__ double wave_sum(const Weights<T> w, int lo, int hi)
 {
     const int lane = threadIdx.x & 63;
     double sum = 0.;
     int v = lo + lane * VE;
-    if (hi - lo >= 4 * STEP) {
-        for (; v <= hi - 3 * STEP - VE; v += 4 * STEP) {
-            Eight x[4], y[4];
+    for (int full = (hi - lo) / (4 * STEP); full > 0; --full, v += 4 * STEP) {
+        Eight x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = load8(w.p + v + i * STEP);
+        if (w.q) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                x[i] = load8(w.p + v + i * STEP);
-            if (w.q) {
+                y[i] = load8(w.q + v + i * STEP);
+        }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
+            sum += sum8(w.combine(v + i * STEP, x[i], y[i]));
+    }
+    if (hi - v >= VE) {
+        Eight x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = y[i] = Eight{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (hi - v >= i * STEP + VE) {
+                x[i] = load8(w.p + v + i * STEP);
+                if (w.q)
                     y[i] = load8(w.q + v + i * STEP);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                sum += sum8(w.combine(v + i * STEP, x[i], y[i]));
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (hi - v >= i * STEP + VE)
+                sum += sum8(w.combine(v + i * STEP, x[i], y[i]));
     }
-    for (; v < hi; v += STEP)
-        sum += sum8(w.at(v, hi));
+    const int end = hi - (hi - lo) % VE;  // the elements left over, fewer than a load's
+    if (end < hi && lane == 0)
+        sum += sum8(w.at(end, hi));
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1)
         sum += __shfl_xor(sum, m);
@@ -191,39 +213,39 @@ __global__ void __launch_bounds__(SUM_THREADS) verify_sum_kernel(const VerifyArg
     }
 }
 
-// The first of `n` sums (LDS or global) at which the running sum from `before` passes `aim`, or
-// where rounding leaves none the last that is not zero (-1: all are). before: up to it.
-__device__ __forceinline__ int find(const double *sums, int n, double aim, double &before)
+// Running sum of n <= 64 values, lane i those of 0 .. i (lanes past n: all of them)
+__device__ __forceinline__ double scan(const double *sums, int n, double &own)
 {
-    double run = before;
-    int at = -1;
-    for (int i = 0; i < n; ++i) {
-        const double x = sums[i];
-        if (x > 0.)
-            at = i, before = run;
-        run += x;
-        if (run > aim && at == i)
-            break;
+    const int lane = threadIdx.x & 63;
+    own = lane < n ? sums[lane] : 0.;
+    double run = own;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const double y = __shfl_up(run, m);
+        run += lane >= m ? y : 0.;
     }
-    return at;
+    return run;
 }
 
 template <typename T, bool PARTS>
 __global__ void __launch_bounds__(PICK_THREADS) verify_pick_kernel(const VerifyArgs a)
 {
-    __shared__ int first;
+    __shared__ int first, hit, last;
     __shared__ double sums[64];
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const float u = a.u[(int64_t)b * (a.T + 1) + a.T];
     int acc, n, nsum = PICK_WAVES;
+    if (tid == 0)
+        hit = 0x7fffffff, last = -1;
     if constexpr (PARTS)
         acc = a.info[2 * b], n = a.info[2 * b + 1];
     else
         acc = accept<T, PICK_THREADS>(a, b, &first, n);
     Weights<T> w(a, b, acc, n);
 
-    // sums of the row's stretches of `per` elements, into sums[0 .. nsum)
     int lo = 0, hi = a.V, per = 0;
+    // sums of 16 stretches of `per` elements of lo .. hi-1
     const auto cut = [&]() {
         per = (hi - lo + PICK_WAVES - 1) / PICK_WAVES;
         per = (per + VE - 1) / VE * VE;
@@ -234,68 +256,82 @@ __global__ void __launch_bounds__(PICK_THREADS) verify_pick_kernel(const VerifyA
         if (lane == 0)
             sums[wave] = s;
         __syncthreads();
-    };
-    const auto total = [&]() {
-        double s = 0.;
-        for (int i = 0; i < nsum; ++i)
-            s += sums[i];
-        return s;
-    };
-    if constexpr (PARTS) {
-        if (tid < a.nseg)
-            sums[tid] = a.part[(int64_t)b * a.nseg + tid];
-        nsum = a.nseg, per = a.seg;
-        __syncthreads();
-    } else
-        cut();
-    double all = total();
-    if (!(all > 0.) && (w.q || w.one_hot >= 0)) {  // nothing is left over: draw from p itself
-        w.q = nullptr, w.one_hot = -1;
         nsum = PICK_WAVES;
-        cut();
-        all = total();
-    }
-    int next = -1;
-    if (all > 0.) {
-        const double aim = (double)a.u[(int64_t)b * (a.T + 1) + a.T] * all;
-        double before = 0.;
-        for (;;) {
-            const int found = find(sums, nsum, aim, before), at = found < 0 ? 0 : found;
-            lo = lo + at * per;
-            hi = hi - lo < per ? hi : lo + per;
-            if (hi - lo <= STEP)
-                break;
-            nsum = PICK_WAVES;
+    };
+    // the same of 8 elements per thread: x, their sum `own`, and its running sum in the wave
+    Eight x;
+    double own, run;
+    const auto load_all = [&]() {
+        x = w.at(lo + tid * VE < hi ? lo + tid * VE : hi, hi);
+        own = sum8(x);
+        run = own;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const double y = __shfl_up(run, m);
+            run += lane >= m ? y : 0.;
+        }
+        __syncthreads();
+        if (lane == 63)
+            sums[wave] = run;
+        __syncthreads();
+        nsum = PICK_WAVES;
+    };
+    double part, upto, all, before = 0.;  // lane i: sum i, and those of 0 .. i
+    bool loaded = false;
+    for (int pass = 0; pass < 2; ++pass) {
+        if (hi <= LAST)
+            load_all(), loaded = true;
+        else if (PARTS && pass == 0) {
+            if (tid < a.nseg)
+                sums[tid] = a.part[(int64_t)b * a.nseg + tid];
+            nsum = a.nseg, per = a.seg;
+            __syncthreads();
+        } else
             cut();
-        }
-        if (wave == 0) {
-            const Eight x = w.at(lo + lane * VE, hi);
-            const double own = sum8(x);
-            double run = own;
+        upto = scan(sums, nsum, part), all = __shfl(upto, 63);
+        if (all > 0. || (!w.q && w.one_hot < 0))
+            break;
+        w.q = nullptr, w.one_hot = -1;  // nothing is left over: draw from p itself
+    }
+    const double aim = (double)u * all;
+    while (hi - lo > LAST) {
+        // the first stretch at which the running sum passes the aim, or where rounding leaves
+        // none the last that is not zero
+        const uint64_t pass = __ballot(part > 0. && before + upto > aim), any = __ballot(part > 0.);
+        const int at = pass ? __builtin_ctzll(pass) : any ? 63 - __builtin_clzll(any) : 0;
+        before += __shfl(upto, at) - __shfl(part, at);
+        lo = lo + at * per;
+        hi = hi - lo < per ? hi : lo + per;
+        if (hi - lo <= LAST)
+            break;
+        cut();
+        upto = scan(sums, nsum, part);
+    }
+    if (!loaded) {
+        load_all();
+        upto = scan(sums, nsum, part);
+    }
+    // element by element: the first weight at which the running sum passes the aim, or the last
+    before += __shfl(upto, wave) - __shfl(part, wave) + (run - own);
+    int my_hit = -1, my_last = -1;
 #pragma unroll
-            for (int m = 1; m < 64; m <<= 1) {
-                const double y = __shfl_up(run, m);
-                run += lane >= m ? y : 0.;
-            }
-            run = before + (run - own);
-            int hit = -1, last = -1;
-#pragma unroll
-            for (int i = 0; i < VE; ++i) {
-                run += x.x[i];
-                if (x.x[i] > 0.f)
-                    last = i;
-                if (hit < 0 && x.x[i] > 0.f && run > aim)
-                    hit = i;
-            }
-            const uint64_t hits = __ballot(hit >= 0), any = __ballot(last >= 0);
-            const int l = hits ? __builtin_ctzll(hits) : any ? 63 - __builtin_clzll(any) : 0;
-            const int i = __shfl(hits ? hit : last, l);
-            next = lo + l * VE + i;
+    for (int i = 0; i < VE; ++i) {
+        before += x[i];
+        if (x[i] > 0.f) {
+            my_last = i;
+            if (my_hit < 0 && before > aim)
+                my_hit = i;
         }
     }
+    const uint64_t hits = __ballot(my_hit >= 0), any = __ballot(my_last >= 0);
+    if (hits && lane == __builtin_ctzll(hits))
+        atomicMin(&hit, lo + tid * VE + my_hit);
+    if (any && lane == 63 - __builtin_clzll(any))
+        atomicMax(&last, lo + tid * VE + my_last);
+    __syncthreads();
     if (tid == 0) {
         a.accepted[b] = acc;
-        a.next[b] = next;
+        a.next[b] = hit != 0x7fffffff ? hit : last;
         if (a.len)
             a.len[b] += acc + 1;
     }
