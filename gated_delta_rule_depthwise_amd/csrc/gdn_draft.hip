@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(THREADS, (draft_waves<DK, DV, KDA, TOK>())) dr
                         *(f32x4 *)(bt + wave * DK + 16 * i + 4 * g4) = ge[i];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        ge[i][j] = dpp<DPP_SHR + 1>(ge[i][j]);
+                        kf[i][j] *= __expf(dpp<DPP_SHR + 1>(ge[i][j]));
                 }
             } else {
                 gs = row_scan(in ? gs : 0.f);
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(THREADS, (draft_waves<DK, DV, KDA, TOK>())) dr
 #pragma unroll
             for (int i = 0; i < DK / 16; ++i) {
                 if constexpr (KDA) {
-                    f32x4 x = ge[i] + load4(run + ws * DK + 16 * i + 4 * g4);
+                    f32x4 x = load4(run + ws * DK + 16 * i + 4 * g4);
                     for (int v = wave - newer; v < wave; ++v)
                         x += load4(bt + v * DK + 16 * i + 4 * g4);
 #pragma unroll

@@ -339,10 +339,11 @@ __global__ void __launch_bounds__(PICK_THREADS) verify_pick_kernel(const VerifyA
 
 template <typename T> hipError_t verify_t(const VerifyArgs &a, hipStream_t s)
 {
-    // Rows of a batch that fills the device, or short ones, are one workgroup's work each;
-    // a workgroup alone draws about 100 bytes per ns, so two rows of 256 KiB cost it about
-    // as much as the second launch of the other way.
-    if (a.B >= 48 || (int64_t)a.V * (int64_t)sizeof(T) <= (256 << 10)) {
+    // One workgroup per row where rows are short or fill the device; a few long rows by parts
+    // and a second launch (1 stream of 131072: 10.3 us against 16.0 us, 96 streams of 200000:
+    // 28.3 us against 41.0 us; 1 stream of 32000: 9.8 us against 9.4 us, 256 streams of 131072:
+    // 47.0 us against 43.4 us).
+    if (a.V <= 32768 || a.B >= 128) {
         hipLaunchKernelGGL((verify_pick_kernel<T, false>), dim3((unsigned)a.B), dim3(PICK_THREADS), 0, s, a);
         return hipGetLastError();
     }
