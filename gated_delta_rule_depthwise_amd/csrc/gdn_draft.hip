@@ -128,20 +128,21 @@ template <int DK, int DV, bool KDA, int TOK> struct DraftShape {
     static constexpr int G = THREADS / DV;     // threads per column
     static constexpr int EG = 16 / G;          // entries of a tape block per thread of a column
     static constexpr int GW = KDA ? DK : 1;    // log-gates per token
+    static constexpr int CQ = DK / WAVES / 16; // 16-channel groups per wave in the scores
     static_assert(G == RS, "a part of Y per thread of a column");
     // LDS, in floats; the partial products Y overlay what is dead by then
     static constexpr int KQ = 0;
     static constexpr int Y = KQ + R * LDK;
-    static constexpr int SP = Y;                              // scores of a block per wave
-    static constexpr int BT = SP + WAVES * R * LDS_;          // log-decay over a wave's block
-    static constexpr int GK = BT + WAVES * GW;                // KDA: new tokens' log-gates
+    static constexpr int SP = Y;                              // a round's scores, by wave
+    static constexpr int FS = SP + 2 * WAVES * R * LDS_;      // and their sums
+    static constexpr int GK = FS + 2 * R * LDS_;              // KDA: new tokens' log-gates
     static constexpr int END1 = GK + (KDA ? TOK * DK : 0);
     static constexpr int END2 = Y + RS * R * DV;
     static constexpr int RUN = END1 > END2 ? END1 : END2;     // log-decay over a tape's newer blocks
     static constexpr int VD = RUN + NS * GW;                  // v
     static constexpr int CO = VD + TOK * DV;                  // coefficients among new tokens
     static constexpr int SM = CO + R * TOK;                   // small: see the kernel
-    static constexpr int TOTAL = SM + 2 * TOK + NS + WAVES;
+    static constexpr int TOTAL = SM + 2 * TOK + NS + 32;
     static_assert(RW % 16 == 0 && DK % 16 == 0, "tile map");
 };
 
@@ -151,7 +152,7 @@ template <int DK, int DV, bool KDA, int TOK> struct DraftShape {
 // 44 us with 3 and spills, 36 us with 2).
 template <int DK, int DV, bool KDA, int TOK> constexpr int draft_waves()
 {
-    return TOK == 16 ? 2 : DK == 64 || (!KDA && DV == 128) ? 4 : KDA ? 2 : 3;
+    return TOK == 16 ? 2 : DK == 64 || (!KDA && DV == 128) ? 4 : 3;
 }
 
 template <typename T, int DK, int DV, bool KDA, int K, int TOK>
@@ -162,13 +163,13 @@ __global__ void __launch_bounds__(THREADS, (draft_waves<DK, DV, KDA, TOK>())) dr
     constexpr int W = K > 0 ? K - 1 : 0;
     constexpr int R = S::R, MT = S::MT, NS = S::NS, LDK = S::LDK, EG = S::EG, GW = S::GW;
     __shared__ __align__(16) float sm[S::TOTAL];
-    float *const kq = sm + S::KQ, *const sp = sm + S::SP, *const bt = sm + S::BT;
+    float *const kq = sm + S::KQ, *const sp = sm + S::SP, *const fs = sm + S::FS;
     float *const gk = sm + S::GK, *const y = sm + S::Y, *const run = sm + S::RUN;
     float *const vd = sm + S::VD, *const co = sm + S::CO;
     float *const gam = sm + S::SM;        // [TOK] log-gates through each new token (GDN)
     float *const bet = gam + TOK;         // [TOK]
     int *const slen = (int *)(bet + TOK); // [NS] tape lengths, -1: stream left out
-    int *const sblk = slen + NS;          // [WAVES] the streams of a round's blocks
+    float *const suf = (float *)(slen + NS);  // [2][16] log-decay after a block's entries (GDN)
 
     const int H = a.H, Hqk = a.Hqk, Tn = a.T, cap = a.tape.cap;
     // the tiles of one state run on one XCD (workgroups go to the 8 XCDs in turn), whose L2
@@ -292,43 +293,46 @@ __global__ void __launch_bounds__(THREADS, (draft_waves<DK, DV, KDA, TOK>())) dr
         }
     }
 
-    // ---- loads of the first tape blocks: a wave's keys and log-gates, a thread's updates ----
-    f32x4 kf[DK / 16], ge[KDA ? DK / 16 : 1];
-    float gs = 0.f, dx[2][EG];
-    int ws = 0, whi = 1;  // the wave's block: stream, one past its newest entry
-    const auto load_keys = [&](int blk) {
-        block_at(blk, ws, whi);
-        const int e = whi - 1 - c16;  // lane c16: the c16-th newest entry of the block
-        const int64_t at = (int64_t)(b0 + ws) * cap + (e > 0 ? e : 0);
-        const float *kp = a.tape.k + (at * Hqk + hq) * DK + 4 * g4;
+    // ---- loads of the first two tape blocks: a wave takes the keys' channels wave*DK/4 on (and
+    // their log-gates), a thread some entries of its column's updates ------------------------
+    constexpr int CQ = S::CQ;
+    const int wc = wave * (DK / WAVES) + 4 * g4;
+    f32x4 kf[2][CQ], ge[KDA ? 2 : 1][CQ];
+    float gs[2], dx[2][EG];
+    int bs[2], bhi[2];  // the blocks' streams, one past their newest entries
+    // lane c16: the c16-th newest entry of a block
+    const auto load_keys = [&](int p, int blk) {
+        block_at(blk, bs[p], bhi[p]);
+        const int e = bhi[p] - 1 - c16;
+        const int64_t at = (int64_t)(b0 + bs[p]) * cap + (e > 0 ? e : 0);
+        const float *kp = a.tape.k + (at * Hqk + hq) * DK + wc;
 #pragma unroll
-        for (int i = 0; i < DK / 16; ++i)
-            kf[i] = load4(kp + 16 * i);
+        for (int i = 0; i < CQ; ++i)
+            kf[p][i] = load4(kp + 16 * i);
         if constexpr (KDA) {
-            const float *gp = a.tape.g + (at * H + head) * DK + 4 * g4;
+            const float *gp = a.tape.g + (at * H + head) * DK + wc;
 #pragma unroll
-            for (int i = 0; i < DK / 16; ++i)
-                ge[i] = load4(gp + 16 * i);
-        } else
-            gs = a.tape.g[at * H + head];
+            for (int i = 0; i < CQ; ++i)
+                ge[p][i] = load4(gp + 16 * i);
+        } else if (wave == 0)
+            gs[p] = a.tape.g[at * H + head];
     };
-    const auto load_updates = [&](int blk, float *d) {
-        int s, hi;
-        block_at(blk, s, hi);
-        const float *dp = a.tape.d + (((int64_t)(b0 + s) * cap + hi - 1) * H + head) * DV + col;
+    const auto load_updates = [&](int p) {
+        const float *dp = a.tape.d + (((int64_t)(b0 + bs[p]) * cap + bhi[p] - 1) * H + head) * DV + col;
 #pragma unroll
         for (int i = 0; i < EG; ++i) {
             const int e = grp * EG + i;  // the block's e-th newest entry
-            d[i] = e < hi ? dp[-(int64_t)e * H * DV] : 0.f;
+            dx[p][i] = e < bhi[p] ? dp[-(int64_t)e * H * DV] : 0.f;
         }
     };
-    constexpr bool EARLY = !KDA || DK == 64;  // registers for the first keys from here on
-    if (EARLY && wave < nblk)
-        load_keys(wave);
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
-        if (p < nblk)
-            load_updates(p, dx[p]);
+    for (int p = 0; p < 2; ++p) {
+        bs[p] = 0, bhi[p] = 1;
+        if (p < nblk) {
+            load_keys(p, p);
+            load_updates(p);
+        }
+    }
 
     // ---- front end ---------------------------------------------------------------------------
     if (tid >= THREADS - TOK) {
@@ -489,139 +493,109 @@ __global__ void __launch_bounds__(THREADS, (draft_waves<DK, DV, KDA, TOK>())) dr
         }
     }
 
-    // ---- the tapes: each round every wave scores one block against all rows; then a thread
-    // per column adds the block's updates to the rows of the block's own stream (so what a
-    // tape holds reaches no other stream, be it NaN) ------------------------------------------
+    // ---- the tapes, two blocks a round: each wave's channels of their scores against all
+    // rows, summed over the waves; then a thread per column adds the blocks' updates to the
+    // rows of their own streams (so what a tape holds reaches no other stream, be it NaN) ------
     float hist[R];
 #pragma unroll
     for (int m = 0; m < R; ++m)
         hist[m] = 0.f;
-    for (int blk0 = 0; blk0 < nblk; blk0 += WAVES) {
-        const bool act = blk0 + wave < nblk;
-        if (!EARLY && act)
-            load_keys(blk0 + wave);
-        if (lane == 0)
-            sblk[wave] = act ? ws : -1;
-        if (act) {  // log-decay over the block's newer entries, and over the whole block
-            const bool in = whi - 1 - c16 >= 0;
+    if (KDA && nblk > 0)
+        __syncthreads();  // the decayed keys and queries
+    for (int blk0 = 0; blk0 < nblk; blk0 += 2) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            if (blk0 + p >= nblk)
+                continue;
+            // the decay after each entry: over the block's newer entries (a scan over the
+            // lanes) and over the tape's newer blocks
+            const bool in = bhi[p] - 1 - c16 >= 0;
             if constexpr (KDA) {
+                float *const rp = run + bs[p] * DK + wc;
 #pragma unroll
-                for (int i = 0; i < DK / 16; ++i) {
+                for (int i = 0; i < CQ; ++i) {
+                    const f32x4 newer = load4(rp + 16 * i);
+                    f32x4 sum;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        ge[i][j] = row_scan(in ? ge[i][j] : 0.f);
-                    if (c16 == 15)
-                        *(f32x4 *)(bt + wave * DK + 16 * i + 4 * g4) = ge[i];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        kf[i][j] *= __expf(dpp<DPP_SHR + 1>(ge[i][j]));
+                    for (int j = 0; j < 4; ++j) {
+                        sum[j] = row_scan(in ? ge[p][i][j] : 0.f);
+                        kf[p][i][j] *= __expf(dpp<DPP_SHR + 1>(sum[j]) + newer[j]);
+                    }
+                    if (c16 == 15)  // this wave alone reads and writes these channels
+                        *(f32x4 *)(rp + 16 * i) = newer + sum;
                 }
-            } else {
-                gs = row_scan(in ? gs : 0.f);
-                if (lane == 15)
-                    bt[wave] = gs;
-                gs = dpp<DPP_SHR + 1>(gs);
+            } else if (wave == 0) {
+                const float sum = row_scan(in ? gs[p] : 0.f), newer = run[bs[p]];
+                if (g4 == 0)
+                    suf[16 * p + c16] = dpp<DPP_SHR + 1>(sum) + newer;
+                if (lane == 15)  // this wave alone writes the sums, and reads them until the state
+                    run[bs[p]] = newer + sum;
             }
-        }
-        __syncthreads();
-        if (act) {
-            // the waves before this one with newer blocks of its stream
-            int newer = (tape_len(ws) - whi) >> 4;
-            newer = newer < wave ? newer : wave;
-            const bool in = whi - 1 - c16 >= 0;
             f32x4 sc[MT];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
                 sc[mt] = zero4();
-            if constexpr (!KDA) {
-                gs += run[ws];
-                for (int v = wave - newer; v < wave; ++v)
-                    gs += bt[v];
-            }
 #pragma unroll
-            for (int i = 0; i < DK / 16; ++i) {
-                if constexpr (KDA) {
-                    f32x4 x = load4(run + ws * DK + 16 * i + 4 * g4);
-                    for (int v = wave - newer; v < wave; ++v)
-                        x += load4(bt + v * DK + 16 * i + 4 * g4);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        kf[i][j] *= __expf(x[j]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < DK / 16; ++i)
+            for (int i = 0; i < CQ; ++i)
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    const f32x4 av = load4(kq + (16 * mt + c16) * LDK + 16 * i + 4 * g4);
+                    const f32x4 av = load4(kq + (16 * mt + c16) * LDK + wc + 16 * i);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        sc[mt] = mfma4(av[j], kf[i][j], sc[mt]);
+                        sc[mt] = mfma4(av[j], kf[p][i][j], sc[mt]);
                 }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int m = 16 * mt + 4 * g4 + r, tok = m % TOK;
-                    float f = 1.f;
-                    if constexpr (!KDA)
-                        f = __expf(gam[tok < nt ? tok : 0] + gs);
-                    sp[(wave * R + m) * S::LDS_ + c16] = in ? sc[mt][r] * f : 0.f;
-                }
+                for (int r = 0; r < 4; ++r)
+                    sp[((p * WAVES + wave) * R + 16 * mt + 4 * g4 + r) * S::LDS_ + c16] = sc[mt][r];
+        }
+        const int s2[2] = {bs[0], bs[1]}, hi2[2] = {bhi[0], bhi[1]};
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+            if (blk0 + 2 + p < nblk)
+                load_keys(p, blk0 + 2 + p);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2 * R * 16 / THREADS; ++i) {
+            const int idx = tid + i * THREADS, e = idx & 15, m = idx / 16 % R, p = idx / (16 * R), tok = m % TOK;
+            float v = 0.f;
+#pragma unroll
+            for (int q = 0; q < WAVES; ++q)
+                v += sp[((p * WAVES + q) * R + m) * S::LDS_ + e];
+            if constexpr (!KDA)
+                v *= __expf(gam[tok] + suf[16 * p + e]);
+            fs[(p * R + m) * S::LDS_ + e] = e < (p ? hi2[1] : hi2[0]) ? v : 0.f;
         }
         __syncthreads();
-        if (EARLY && blk0 + WAVES + wave < nblk)
-            load_keys(blk0 + WAVES + wave);
-        // the log-decay over the blocks so far, for the next round and the state
-        if constexpr (KDA) {
-            if (tid < DK) {
-                float add[WAVES];
 #pragma unroll
-                for (int v = 0; v < WAVES; ++v)
-                    add[v] = bt[v * DK + tid];
-                for (int v = 0; v < WAVES && blk0 + v < nblk; ++v)
-                    run[sblk[v] * DK + tid] += add[v];
-            }
-        } else if (tid < NS) {
-            float sum = run[tid];
+        for (int p = 0; p < 2; ++p) {
+            if (blk0 + p >= nblk)
+                continue;
+            const int lo = s2[p] * Tn, up = lo + Tn;
+            const float *xp = fs + p * R * S::LDS_ + grp * EG;
 #pragma unroll
-            for (int v = 0; v < WAVES; ++v)
-                sum += sblk[v] == tid ? bt[v] : 0.f;
-            run[tid] = sum;
-        }
-        for (int v0 = 0; v0 < WAVES && blk0 + v0 < nblk; v0 += 2) {
-            if (blk0 + v0 > 0) {
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    if (blk0 + v0 + p < nblk)
-                        load_updates(blk0 + v0 + p, dx[p]);
-            }
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                if (blk0 + v0 + p >= nblk)
+            for (int m = 0; m < TOK; ++m) {
+                if (m < lo || m >= up)
                     continue;
-                int s, hi;
-                block_at(blk0 + v0 + p, s, hi);
-                const int lo = s * Tn, up = lo + Tn;
-                const float *xp = sp + (v0 + p) * R * S::LDS_ + grp * EG;
 #pragma unroll
-                for (int m = 0; m < TOK; ++m) {
-                    if (m < lo || m >= up)
-                        continue;
+                for (int i = 0; i < EG; i += 4) {
+                    const f32x4 xk = load4(xp + m * S::LDS_ + i), xq = load4(xp + (TOK + m) * S::LDS_ + i);
 #pragma unroll
-                    for (int i = 0; i < EG; i += 4) {
-                        const f32x4 xk = load4(xp + m * S::LDS_ + i), xq = load4(xp + (TOK + m) * S::LDS_ + i);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            hist[m] += xk[j] * dx[p][i + j];
-                            hist[TOK + m] += xq[j] * dx[p][i + j];
-                        }
+                    for (int j = 0; j < 4; ++j) {
+                        hist[m] += xk[j] * dx[p][i + j];
+                        hist[TOK + m] += xq[j] * dx[p][i + j];
                     }
                 }
             }
         }
-        __syncthreads();
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+            if (blk0 + 2 + p < nblk)
+                load_updates(p);
     }
+    if (nblk > 0)
+        __syncthreads();
 
     // ---- the state, 64 columns and RW rows per wave: lane (g4, c16) loads 4 adjacent columns
     // of the rows 4 g4 + i, which serve 4 products of 16 columns each ------------------------
