@@ -146,13 +146,12 @@ template <int DK, int DV, bool KDA, int TOK> struct DraftShape {
     static_assert(RW % 16 == 0 && DK % 16 == 0, "tile map");
 };
 
-// Waves per SIMD the registers are held to: with fewer tokens and the scalar gate four
-// workgroups of a CU hide each other's waits (256 streams x 8 tokens: 174 us with 4, 188 us
-// with 3); the channel gates' factors and the wide instances would spill there (32 x 4 tokens:
-// 44 us with 3 and spills, 36 us with 2).
+// Waves per SIMD the registers are held to: four workgroups of a CU hide each other's waits
+// (256 streams x 8 tokens: 169 us with 4, 183 us with 3; channel gates, 32 x 4 tokens: 29.4 us
+// with 4 and 18 registers spilled, 32.3 us with 3). Twice the tokens take the LDS of two.
 template <int DK, int DV, bool KDA, int TOK> constexpr int draft_waves()
 {
-    return TOK == 16 ? 2 : DK == 64 || (!KDA && DV == 128) ? 4 : 3;
+    return TOK == 16 ? 2 : DV <= 128 ? 4 : 3;
 }
 
 template <typename T, int DK, int DV, bool KDA, int K, int TOK>
