@@ -863,7 +863,8 @@ int check_tape(const gdn_params *p, int kda, const gdn_tape *t, int32_t B, int32
         return rc;
     if (!((p->dk == 64 || p->dk == 128) && (p->dv == p->dk || p->dv == 2 * p->dk)))
         return GDN_E_UNSUPPORTED;
-    if (B < 1 || share < 1 || B % share || (int64_t)B * p->H > (int64_t)INT32_MAX)
+    // the grids (up to 4 workgroups of 256 threads per stream and head) stay below 2^32 threads
+    if (B < 1 || share < 1 || B % share || (int64_t)B * p->H > (1 << 22))
         return GDN_E_ARG;
     if (!t || !t->k || !t->d || !t->g || !t->len || t->cap < 1 ||
         (p->conv_k > 0) != (t->raw != nullptr))
@@ -887,7 +888,7 @@ int draft(const gdn_params *p, int kda, const void *q, const void *k, const void
     const int rc = check_tape(p, kda, tape, B, share);
     if (rc != GDN_OK)
         return rc;
-    if (T < 1 || T > GDN_DRAFT_MAX_T || T > tape->cap || (int64_t)B * T > (int64_t)INT32_MAX)
+    if (T < 1 || T > GDN_DRAFT_MAX_T || T > tape->cap)
         return GDN_E_ARG;
     if (!q || !k || !v || !g || !beta || !h_ptrs || !o)
         return GDN_E_ARG;
@@ -933,7 +934,8 @@ int fold(const gdn_params *p, int kda, const float *const *h_ptrs,
     const bool front = p->conv_k > 0;
     if (front != (conv_state_ptrs != nullptr) || front != (conv_out_ptrs != nullptr))
         return GDN_E_ARG;
-    if (share > 1 && (const void *)h_ptrs == (const void *)h_out_ptrs)
+    if (share > 1 && ((const void *)h_ptrs == (const void *)h_out_ptrs ||
+                      (front && (const void *)conv_state_ptrs == (const void *)conv_out_ptrs)))
         return GDN_E_ARG;  // the streams of a state have states of their own after it
     gdn::FoldArgs a{};
     a.dbg = debug_status.load();
@@ -952,12 +954,12 @@ int fold(const gdn_params *p, int kda, const float *const *h_ptrs,
 
 // The parts a row of weights is cut into: multiples of 8192 elements (four rounds of loads
 // of a workgroup's 4 waves) and at most 64 of them.
-constexpr int32_t kVerifySeg = 8192, kVerifyParts = 64, kVerifyMaxT = 1024, kVerifyMaxV = 1 << 30;
+constexpr int32_t kVerifySeg = 8192, kVerifyParts = 64, kVerifyMaxT = 1024, kVerifyMaxV = 1 << 30,
+                  kVerifyMaxB = 1 << 18;
 
 bool verify_shape(int32_t B, int32_t T, int32_t V, int32_t *nseg, int32_t *seg)
 {
-    if (B < 1 || T < 0 || T > kVerifyMaxT || V < 1 || V > kVerifyMaxV ||
-        (int64_t)B * kVerifyParts > (int64_t)INT32_MAX)
+    if (B < 1 || T < 0 || T > kVerifyMaxT || V < 1 || V > kVerifyMaxV || B > kVerifyMaxB)
         return false;
     int64_t s = ((int64_t)V + kVerifyParts - 1) / kVerifyParts;
     s = (s + kVerifySeg - 1) / kVerifySeg * kVerifySeg;

@@ -731,6 +731,17 @@ __global__ void __launch_bounds__(THREADS, (draft_waves<DK, DV, KDA, TOK>())) dr
 // is taken in blocks of 16 entries, oldest first: the state times the block's decay, plus the
 // block's entries with the decay after each (summed from the newest back: no differences of
 // long sums). A block's loads go out while the one before is worked in.
+//
+// The accumulators cross the loop's edges; the wait states that an MFMA result needs before
+// another instruction reads it are kept there by hand (settle), since along a branch the
+// compiler has placed too few of them before.
+__device__ __forceinline__ void settle()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 7\n\ts_nop 7");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 template <typename T, int DK, int DV, bool KDA, int SL>
 __global__ void __launch_bounds__(THREADS, SL == 64 ? 4 : 3) fold_kernel(const FoldArgs a)
 {
@@ -868,6 +879,7 @@ __global__ void __launch_bounds__(THREADS, SL == 64 ? 4 : 3) fold_kernel(const F
                 for (int j = 0; j < 4; ++j)
                     acc[rt][j] = mfma4(k, dv[q][j], acc[rt][j]);
             }
+        settle();
         if (eb + EB < n)
             load_entries(eb + EB);
     }

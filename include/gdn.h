@@ -293,8 +293,9 @@ typedef struct gdn_tape {
  *                   state, 16-byte aligned; stream b reads h_ptrs[b / share].
  *   conv_state_ptrs device array of B/share device pointers to [cd][conv_k-1] windows: the
  *                   raw inputs before the tape's first entry (NULL iff conv_k == 0).
- *   share           consecutive streams per state; B must be a multiple of it. The state is
- *                   read once for as many of its streams' tokens as a workgroup holds.
+ *   share           consecutive streams per state; B must be a multiple of it, and B * H at
+ *                   most 2^22. A workgroup reads the state once for up to 8 of its streams (8
+ *                   tokens in all, 16 when T > 8); the others find it in their XCD's L2.
  *   o               [B*T][H][dv] float32, out (16-byte aligned).
  * A stream with len[b] < 0 or len[b] + T > cap is left out: none of its rows of o nor entries
  * are written (with gdn_debug_validate on, GDN_BAD_TAPE is set); the others are not affected.
@@ -361,7 +362,7 @@ int kda_fold(const gdn_params *p, const float *const *h_ptrs,
  *              accepted drafts and the token before them (a gdn_draft call over the T+1 rows
  *              of that token and its drafts gave the target's T+1 rows).
  *   ws         >= gdn_verify_workspace_bytes(B, T, V), 16-byte aligned.
- * 0 <= T <= 1024, 1 <= V <= 2^30, ld >= V. Sums are held in float64; weights that are negative
+ * B <= 2^18, 0 <= T <= 1024, 1 <= V <= 2^30, ld >= V. Sums are held in float64; weights that are negative
  * or NaN count as zero. Only rows a of the probabilities are read whole. One launch, or two
  * for a few streams with long rows.
  */

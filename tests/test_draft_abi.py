@@ -53,7 +53,7 @@ def test_draft_refusals(fn):
                dict(q=F + 2), dict(t=tape(cap=0)), dict(t=tape(cap=3)), dict(t=tape(k=None)),
                dict(t=tape(d=None)), dict(t=tape(g=None)), dict(t=tape(len=None)), dict(t=tape(k=F + 4)),
                dict(t=tape(d=F + 8)), dict(t=tape(raw=F)), dict(cs=F), dict(cw=F),
-               dict(n=1 << 30, T=16), dict(n=(1 << 31) - 1, params=B.params(2, 64, 64))):
+               dict(n=1 << 30, T=16), dict(n=(1 << 21) + 1)):
         refused(**kw)
     if fn is B.kda_draft:
         refused(g=F + 4)
@@ -86,11 +86,13 @@ def test_fold_refusals(fn):
         assert fold(p, fn=fn, **kw) == B.GDN_E_ARG, kw
     for kw in (dict(), dict(cs=F), dict(co=F), dict(cs=F, co=F), dict(cs=F, t=tape(raw=F))):
         assert fold(front, fn=fn, **kw) == B.GDN_E_ARG, kw
+    assert fold(front, fn=fn, cs=F, co=F, t=tape(raw=F), share=2) == B.GDN_E_ARG   # nor shared windows
     assert fold(B.params(2, 64, 128), fn=fn) == B.GDN_E_UNSUPPORTED
 
 
 def test_verify_workspace_and_refusals():
     assert B.gdn_verify_workspace_bytes(0, 1, 10) == 0
+    assert B.gdn_verify_workspace_bytes((1 << 18) + 1, 1, 10) == 0
     assert B.gdn_verify_workspace_bytes(1, -1, 10) == 0
     assert B.gdn_verify_workspace_bytes(1, 1025, 10) == 0
     assert B.gdn_verify_workspace_bytes(1, 1, 0) == 0
