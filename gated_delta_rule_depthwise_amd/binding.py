@@ -36,7 +36,7 @@ EXPORTS = ("gdn_prefill", "gdn_prefill_noalloc", "gdn_noalloc_scratch_bytes", "k
            "gdn_verify", "gdn_verify_workspace_bytes")
 GDN_BAD_CU_START, GDN_BAD_CU_ORDER, GDN_BAD_CU_TOTAL, GDN_BAD_CU_MAXLEN = 1, 2, 4, 8
 GDN_BAD_KDA_GATE = 16
-GDN_BAD_TAPE = 32
+GDN_BAD_TAPE = 1
 GDN_DRAFT_MAX_T = 16
 GDN_PROF_FRONT = 0
 GDN_PROF_RECUR = 1
@@ -56,7 +56,8 @@ class gdn_params(ctypes.Structure):
 
 class gdn_tape(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("d", ctypes.c_void_p), ("g", ctypes.c_void_p),
-                ("raw", ctypes.c_void_p), ("len", ctypes.c_void_p), ("cap", ctypes.c_int32)]
+                ("raw", ctypes.c_void_p), ("len", ctypes.c_void_p), ("cap", ctypes.c_int32),
+                ("status", ctypes.c_void_p)]
 
 
 _vp = ctypes.c_void_p
@@ -214,10 +215,10 @@ def kda_decode(p, q, k, v, g, beta, h_ptrs, conv_state_ptrs, conv_w, o, B, strea
                              _p(h_ptrs), _p(conv_state_ptrs), _p(conv_w), _p(o), B, stream)
 
 
-def tape(k, d, g, raw, len, cap):
-    """A gdn_tape struct over device tensors or pointers (raw None without the conv). It
-    holds no references: the tensors must outlive its use."""
-    return gdn_tape(_p(k), _p(d), _p(g), _p(raw), _p(len), cap)
+def tape(k, d, g, raw, len, cap, status=None):
+    """A gdn_tape struct over device tensors or pointers (raw None without the conv; status
+    a device int32 or None). It holds no references: the tensors must outlive its use."""
+    return gdn_tape(_p(k), _p(d), _p(g), _p(raw), _p(len), cap, _p(status))
 
 
 def gdn_draft(p, q, k, v, g, beta, h_ptrs, conv_state_ptrs, conv_w, tape, o, B, T, share,

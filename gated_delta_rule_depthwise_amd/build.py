@@ -12,7 +12,7 @@ INCLUDE = os.path.join(ROOT, "include")
 SO = os.path.join(PKG, "libgdn.so")
 SOURCES = [os.path.join(CSRC, "gdn_kernels.hip"), os.path.join(CSRC, "gdn_decode.hip"),
            os.path.join(CSRC, "gdn_draft.hip"), os.path.join(CSRC, "gdn_verify.hip"),
-           os.path.join(CSRC, "gdn_api.cpp")]
+           os.path.join(CSRC, "gdn_api.cpp"), os.path.join(CSRC, "gdn_draft_api.cpp")]
 
 
 def hipcc() -> str:

@@ -17,7 +17,7 @@
 #include <stdint.h>
 
 #include "gdn.h"
-#include "gdn_internal.h"
+#include "gdn_draft.h"
 
 namespace gdn {
 
@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(THREADS, (draft_waves<DK, DV, KDA, TOK>())) dr
     }
     if (tid < NS) {
         slen[tid] = len_s;
-        if (tid < ns && len_s < 0 && a.dbg && head == 0)
-            atomicOr(a.dbg, GDN_BAD_TAPE);
+        if (tid < ns && len_s < 0 && a.tape.status && head == 0)
+            atomicOr(a.tape.status, GDN_BAD_TAPE);
     }
     const auto tape_len = [&](int s) { return __builtin_amdgcn_readlane(len_s, s); };
     const int nb_s = (len_s + 15) >> 4;
@@ -764,8 +764,8 @@ __global__ void __launch_bounds__(THREADS, SL == 64 ? 4 : 3) fold_kernel(const F
     const bool bad = n < 0 || n > cap;
     const bool on = !bad && n >= a.min_len;
     if (head == 0 && slice == 0 && tid == 0) {
-        if (bad && a.dbg)
-            atomicOr(a.dbg, GDN_BAD_TAPE);
+        if (bad && a.tape.status)
+            atomicOr(a.tape.status, GDN_BAD_TAPE);
         if (a.len_out && a.len_out != a.tape.len)
             a.len_out[b] = on ? 0 : n;
     }

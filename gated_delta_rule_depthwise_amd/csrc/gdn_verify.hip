@@ -13,7 +13,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "gdn_internal.h"
+#include "gdn_draft.h"
 
 namespace gdn {
 

@@ -202,6 +202,7 @@ class Drafts:
         self.raw = None if self.conv_w is None else torch.full(
             (B_, cap, spec.cd), fill, dtype=td, device=device)
         self.len = torch.zeros(B_, dtype=torch.int32, device=device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
         self.h_ptrs = self._ptrs(self.h)
         self.cs_ptrs = None if self.conv_state is None else self._ptrs(self.conv_state)
 
@@ -210,7 +211,7 @@ class Drafts:
                             device=self.device)
 
     def tape(self):
-        return B.tape(self.k, self.d, self.g, self.raw, self.len, self.cap)
+        return B.tape(self.k, self.d, self.g, self.raw, self.len, self.cap, self.status)
 
     def params(self, ld=None, z=None, ld_z=None):
         sp = self.spec

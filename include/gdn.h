@@ -280,7 +280,10 @@ typedef struct gdn_tape {
                      conv_k == 0): the conv reads the last conv_k-1 of them                 */
     int32_t *len; /* [B] entries in use                                                     */
     int32_t cap;  /* entries per stream, >= 1                                               */
+    int32_t *status; /* NULL, or one int32: a call ORs GDN_BAD_TAPE into it when it leaves a
+                        stream out because its length is out of range                      */
 } gdn_tape;
+#define GDN_BAD_TAPE 1
 
 /*
  * T new tokens per stream (1 <= T <= GDN_DRAFT_MAX_T) after the entries of the stream's tape.
@@ -298,10 +301,11 @@ typedef struct gdn_tape {
  *                   tokens in all, 16 when T > 8); the others find it in their XCD's L2.
  *   o               [B*T][H][dv] float32, out (16-byte aligned).
  * A stream with len[b] < 0 or len[b] + T > cap is left out: none of its rows of o nor entries
- * are written (with gdn_debug_validate on, GDN_BAD_TAPE is set); the others are not affected.
+ * are written (and GDN_BAD_TAPE goes into tape->status); the others are not affected.
  * Tokens see only themselves and what came before: NaN in a row, a stream or in entries past
  * len[b] reaches nothing else. Arithmetic is fp32 throughout. KDA gates must be a decay.
- * (dk, dv) as for gdn_decode. No workspace; one kernel, in GDN_PROF_RECUR when profiling.
+ * (dk, dv) as for gdn_decode. No workspace; one kernel. The calls of this section are not
+ * among those that gdn_profile_enable and gdn_debug_validate act on.
  */
 #define GDN_DRAFT_MAX_T 16
 int gdn_draft(const gdn_params *p, const void *q, const void *k, const void *v,
@@ -486,8 +490,6 @@ int gdn_segment_plan(const gdn_params *p, int32_t kind, int32_t B, int64_t t_per
 #define GDN_BAD_CU_TOTAL 4   /* cu_seqlens[B] != total_tokens                          */
 #define GDN_BAD_CU_MAXLEN 8  /* a stream longer than max_seqlen                        */
 #define GDN_BAD_KDA_GATE 16  /* a per-key-channel log-gate above 0 or NaN, in a real row */
-#define GDN_BAD_TAPE 32      /* gdn_draft / gdn_fold: a tape length out of range (the stream
-                                was left out; the call's other streams ran)              */
 int gdn_debug_validate(int32_t *status);
 
 /*
