@@ -7,12 +7,21 @@
 //   d_t = beta_t (v_t - y_t),
 //   o_t = h^T (e^{G_t} q_t) + sum_{j up to t} (k_j . e^{G_t - G_j} q_t) d_j,
 // so the state is read once for all the tokens (and streams) of a workgroup and never
-// written: the whole call moves about half the bytes of one in-place decode step. The
-// products with h, with the tape's keys and with its updates run on fp32 MFMA; the part
-// among the new tokens is a triangular solve of at most 16 steps per column.
+// written: with short tapes the call moves about half the bytes of an in-place decode step.
+// The products with h and with the tape's keys run on fp32 MFMA (a workgroup's 256 products
+// of 16 x 16 x 4 with a 128 x 128 state take 2048 cycles of each SIMD, its 64 KiB about 7000
+// cycles of the CU's share of HBM; operands of fewer bits would need three products each for
+// fp32's precision); the tape's updates are added per column on the VALU, where a stream's
+// rows can be kept apart, and the part among the new tokens is a triangular solve of at most
+// 16 steps per column. HBM bounds the large calls (256 streams x 8 tokens x 32 heads of 128 x
+// 128: 169 us, 842 MB, 5.0 TB/s, where a device copy reaches 5.2); between those and the small
+// ones a workgroup's chain of waits does (rows, L2, scores, products, solve: about 30 000
+// cycles, four workgroups per CU; 64 streams x 5 tokens: 45 us, 4.3 TB/s), and the smallest
+// take one such chain (1 stream x 1 token: 8.7 us).
 //
 // fold: h_out = diag(e^{G_n}) h + sum_j diag(e^{G_n - G_j}) k_j d_j^T, a rank-n update on
-// fp32 MFMA of a state that is read and written once.
+// fp32 MFMA of a state that is read and written once: bound by HBM (64 streams x 32 heads,
+// tapes of 1 to 16: 57 us, 300 MB, 5.2 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -9,7 +9,10 @@
 // (which come from L2 then), 8 per thread, whose running sum gives the token. Where a few
 // streams have long rows (launch_verify), workgroups sum parts of the rows side by side first
 // (verify_sum_kernel). Sums are held in float64 and taken in a fixed order, so the token
-// depends on nothing but the inputs.
+// depends on nothing but the inputs. Measured: 256 streams of 131072 bf16 weights 27 us (a
+// workgroup per CU, so the tests before a row and the search after it are not hidden; the rows
+// alone take about 20 us at 5.2 TB/s), one stream of 32000 weights 9.5 us (four round trips
+// to memory in a chain: drafts, their probabilities, the row, the stretch again).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -244,6 +244,9 @@ FOLDS = {
     "kda shared": dict(B=4, gate="kda", share=2, H=4, Hqk=2, dk=64, dv=64, lens=[1, 2, 17, 0], cap=20),
     "kda strong": dict(B=2, gate="kda", lens=[17, 40], cap=40, dist="strong"),
     "kda wide": dict(B=1, H=1, dv=256, gate="kda", lens=[18], cap=20),
+    "kda many heads": dict(B=32, H=32, gate="kda", lens=[i % 4 for i in range(31)] + [18], cap=18),
+    "kda many wide heads": dict(B=16, H=64, Hqk=32, dv=256, gate="kda", lens=[i % 3 for i in range(16)], cap=2),
+    "many heads": dict(B=32, H=32, lens=[i % 3 for i in range(32)], cap=2),
 }
 
 

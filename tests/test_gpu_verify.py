@@ -55,11 +55,12 @@ def test_draft_counts(B, T):
     check(p, tok, u, q if T else None, num=num)
 
 
+@pytest.mark.parametrize("V", [1000, 9000, 40000])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-def test_borders(dtype):
+def test_borders(dtype, V):
     """The random numbers' ends, a proposal equal to the target (nothing is left over), rows
     without weight, and weights that are NaN, negative or infinite."""
-    p, q, tok, u = make(6, 2, 1000, 9, dtype)
+    p, q, tok, u = make(6, 2, V, 9, dtype)
     u[0], u[1] = 0.0, 1 - 2.0 ** -24
     q[2] = p[2, :2]
     tok[2] = p[2, :2].float().argmax(-1).to(torch.int32)
@@ -74,10 +75,17 @@ def test_borders(dtype):
     check(p, tok, u)
 
 
+def test_a_batch_of_long_rows():
+    """Rows of more than one part in a batch that takes one workgroup each."""
+    p, q, tok, u = make(130, 1, 40001, 19, torch.bfloat16)
+    check(p, tok, u, q)
+
+
 def test_weight_in_one_place():
     """All the weight on the first, the last, or a token in the middle of a part."""
-    for at in (0, 1, 4095, 4096, 5000, 8999):
-        p = torch.zeros(2, 1, 9000, device="cuda")
+    for V, at in ((9000, 0), (9000, 1), (9000, 4095), (9000, 4096), (9000, 8999), (7, 6), (8192, 8191),
+                  (8193, 8192), (40000, 8191), (40000, 8192), (40000, 39999)):
+        p = torch.zeros(2, 1, V, device="cuda")
         p[:, 0, at] = 0.25
         u = torch.tensor([[0.0], [1 - 2.0 ** -24]], device="cuda")
         _, n = check(p, torch.zeros(2, 0, dtype=torch.int32, device="cuda"), u)
