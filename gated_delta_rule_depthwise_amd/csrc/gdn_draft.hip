@@ -153,6 +153,7 @@ template <int DK, int DV, bool KDA, int TOK> struct DraftShape {
     static constexpr int SM = CO + R * TOK;                   // small: see the kernel
     static constexpr int TOTAL = SM + 2 * TOK + NS + 32;
     static_assert(RW % 16 == 0 && DK % 16 == 0, "tile map");
+    static_assert(TOTAL * 4 <= 80 * 1024, "LDS of two workgroups per CU (160 KiB)");
 };
 
 // Waves per SIMD the registers are held to: four workgroups of a CU hide each other's waits
